@@ -3,6 +3,7 @@
 #include <cstdint>
 
 #include "moe_common.cuh"
+#include "moeskew_train.h"
 
 namespace moe {
 
@@ -12,10 +13,6 @@ int num_sms() {
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
   return n > 0 ? n : 1;
 }
-
-namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Checks shared by every stage.
 int check_cfg(const moe_cfg* c) {
@@ -35,9 +32,6 @@ int check_ptrs(std::initializer_list<const void*> ps) {
   return MOE_OK;
 }
 
-int cuda_result(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
-}  // namespace
 }  // namespace moe
 
 using namespace moe;
@@ -171,6 +165,7 @@ const char* moe_status_string(int code) {
     case MOE_STATUS_NONFINITE: return "non-finite router logit";
     case MOE_STATUS_TIMEOUT: return "bounded wait in a kernel ran out";
     case MOE_STATUS_PLAN: return "block plan exceeds its bound";
+    case MOET_STATUS_BAD_SEQ: return "sequence offsets fall or leave the batch";
     default: return code > 0 ? "several device status bits" : "unknown code";
   }
 }

@@ -75,8 +75,6 @@ int scratch_on_current_device(void** out) {
   return MOE_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 }  // namespace
 }  // namespace moe
 

@@ -4,6 +4,7 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include "moeskew.h"
@@ -160,5 +161,12 @@ cudaError_t launch_bwd_wide(const moe_cfg& c, int kind, const uint16_t* a_src,
                             int32_t* status, cudaStream_t st);
 
 int num_sms();
+
+// ---- argument checks of the C ABI's entry points (api.cu) ----
+int check_cfg(const moe_cfg* c);
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// none NULL, all 16-byte aligned
+int check_ptrs(std::initializer_list<const void*> ps);
+inline int cuda_result(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 }  // namespace moe

@@ -1,0 +1,108 @@
+// Shared by the training operators (moeskew_train.h): launchers, 8- and 4-element loads and
+// stores in fp32 from either element type, and launches that overlap their predecessor.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "moe_common.cuh"
+#include "moeskew_train.h"
+
+namespace moe {
+
+// ---- launchers, called by the C ABI after validation ----
+size_t balance_workspace_bytes(const moe_cfg& c, int n_seq);
+cudaError_t launch_balance_loss(const moe_cfg& c, const float* logits, const int32_t* ids,
+                                const uint8_t* mask, const int32_t* seq_off, int n_seq,
+                                float* losses, int32_t* counts, float* probs,
+                                int32_t* seq_info, float* lse, void* ws, int32_t* status,
+                                cudaStream_t st);
+cudaError_t launch_router_backward(const moe_cfg& c, const float* logits, const int32_t* ids,
+                                   const float* gates, const float* dy, const uint16_t* o,
+                                   const int32_t* tok_row, const uint8_t* mask,
+                                   const int32_t* seq_off, int n_seq, const int32_t* counts,
+                                   const int32_t* seq_info, const float* lse,
+                                   const float* dloss, float* dgates, float* dlogits,
+                                   int32_t* status, cudaStream_t st);
+size_t norm_bwd_workspace_bytes(const moe_cfg& c);
+cudaError_t launch_block_norm(const moe_cfg& c, const moet_norm& n, const void* h,
+                              const float* y, const float* gate, const void* w_post,
+                              const void* w_next, void* h_out, uint16_t* x, cudaStream_t st);
+cudaError_t launch_block_norm_backward(const moe_cfg& c, const moet_norm& n,
+                                       const void* h_out, const float* y, const float* gate,
+                                       const void* w_post, const void* w_next,
+                                       const void* dh_out, const float* dx, void* dh,
+                                       float* dy, float* dgate, float* dw_post,
+                                       float* dw_next, void* ws, cudaStream_t st);
+cudaError_t launch_adamw(const moet_adamw_tensor* tensors, int count, const moet_adamw& opt,
+                         const float* lr, const float* grad_scale, int32_t* step,
+                         cudaStream_t st);
+
+// ---- element access ----
+__device__ __forceinline__ void load8(const float* p, float* v) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0];
+  const float4 b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void bf16x8_to_f32(const uint4 a, float* v) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
+  bf16x8_to_f32(*reinterpret_cast<const uint4*>(p), v);
+}
+__device__ __forceinline__ void store8(float* p, const float* v) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                 pack_bf16x2(v[6], v[7]));
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+  return v;
+}
+
+// ---- launches that overlap their predecessor's end (programmatic dependent launch) ----
+// The dependent kernel calls wait_for_predecessor() before it touches what the kernels
+// before it wrote; that returns once the predecessor has ended and its writes are visible.
+__device__ __forceinline__ void wait_for_predecessor() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_successor_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class... KArgs, class... Args>
+cudaError_t launch_after(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                         cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+}  // namespace moe

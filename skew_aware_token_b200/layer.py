@@ -187,6 +187,18 @@ class MoeLayer:
                                   stream)
         return self.view("dx"), self.view("dw1"), self.view("dw2")
 
+    def router_backward(self, router, logits, dy, dloss=None, token_mask=None, seq_off=None,
+                        stream=None):
+        """Gradient of the router's logits for dL/dy = dy after a forward call of this layer
+        that wrote O rows, plus that of `router`'s losses (train.RouterLoss) with dloss:
+        dlogits fp32 [T, E], a view of router's buffer."""
+        if self.o is None or not self.o_rows:
+            raise ValueError("the gates' gradient reads the expert output rows: build the "
+                             "layer with o_rows=True")
+        return router.backward(logits, self.topk_ids, self.topk_gates, dloss=dloss, dy=dy,
+                               o=self.o, tok_row=self.tok_row, token_mask=token_mask,
+                               seq_off=seq_off, stream=stream)
+
     def forward_host(self, logits_h, x_h, w1, w2, y_h, logits_d, x_d, mode=0, stream=None):
         """End to end from pinned host buffers: copies logits and x in, runs the layer,
         copies y out (all asynchronous on the current stream)."""

@@ -228,3 +228,97 @@ def moe_expert_ffn_noalloc(cfg, xp, w1, w2, tiles, plan_info, row_token, row_gat
         ctypes.byref(c), _dev(xp, "xp"), _dev(w1, "w1"), _dev(w2, "w2"), _dev(tiles, "tiles"),
         _dev(plan_info, "plan_info"), _dev(row_token, "row_token"), _dev(row_gate, "row_gate"),
         int(mode), _dev(out, "out"), _dev(status, "status"), _stream(stream)))
+
+
+# ---- the training operators (include/moeskew_train.h) ----
+TRAIN_HEADER_PATH = os.path.join(os.path.dirname(HEADER_PATH), "moeskew_train.h")
+MOET_F32, MOET_BF16, MOET_E4M3 = 0, 1, 2
+MOET_STATUS_BAD_SEQ = 32
+MOET_WS_BALANCE, MOET_WS_NORM_BWD = 0, 1
+MOET_MAX_NORM_D = 8192
+MOET_ADAMW_BLOCK = 256
+
+
+class MoetNorm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_float) for n in ("eps", "w_offset", "res_scale", "out_scale")] + \
+               [(n, ctypes.c_int32) for n in ("h_dtype", "w_dtype")]
+
+
+class MoetAdamwTensor(ctypes.Structure):
+    _fields_ = [(n, _VP) for n in ("p", "g", "m", "v", "m_scale", "v_scale", "master")] + \
+               [("n", ctypes.c_int64), ("weight_decay", ctypes.c_float)] + \
+               [(n, ctypes.c_int32) for n in ("p_dtype", "g_dtype", "state_dtype")]
+
+
+class MoetAdamw(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("beta1", "beta2", "eps")]
+
+
+_SIGNATURES.update({
+    "moet_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(MoeCfg), ctypes.c_int32,
+                                              ctypes.c_int]),
+    "moet_balance_loss": (ctypes.c_int, [ctypes.POINTER(MoeCfg)] + [_VP] * 4 +
+                          [ctypes.c_int32] + [_VP] * 8),
+    "moet_router_backward": (ctypes.c_int, [ctypes.POINTER(MoeCfg)] + [_VP] * 8 +
+                             [ctypes.c_int32] + [_VP] * 8),
+    "moet_block_norm": (ctypes.c_int, [ctypes.POINTER(MoeCfg), ctypes.POINTER(MoetNorm)] +
+                        [_VP] * 8),
+    "moet_block_norm_backward": (ctypes.c_int, [ctypes.POINTER(MoeCfg),
+                                                ctypes.POINTER(MoetNorm)] + [_VP] * 14),
+    "moet_adamw_step": (ctypes.c_int, [ctypes.POINTER(MoetAdamwTensor), ctypes.c_int32,
+                                       ctypes.POINTER(MoetAdamw)] + [_VP] * 4),
+})
+
+
+def moet_workspace_size(cfg, n_seq: int, which: int) -> int:
+    return int(lib().moet_workspace_size(ctypes.byref(_cfg(cfg)), n_seq, which))
+
+
+def moet_balance_loss(cfg, logits, topk_ids, token_mask, seq_off, n_seq, losses, counts, probs,
+                      seq_info, lse, workspace, status, stream=None) -> None:
+    c = _cfg(cfg)
+    _check("moet_balance_loss", lib().moet_balance_loss(
+        ctypes.byref(c), _dev(logits, "logits"), _dev(topk_ids, "topk_ids"),
+        _dev(token_mask, "token_mask"), _dev(seq_off, "seq_off"), int(n_seq),
+        _dev(losses, "losses"), _dev(counts, "counts"), _dev(probs, "probs"),
+        _dev(seq_info, "seq_info"), _dev(lse, "lse"), _dev(workspace, "workspace"),
+        _dev(status, "status"), _stream(stream)))
+
+
+def moet_router_backward(cfg, logits, topk_ids, topk_gates, dy, o, tok_row, token_mask, seq_off,
+                         n_seq, counts, seq_info, lse, dloss, dgates, dlogits, status,
+                         stream=None) -> None:
+    c = _cfg(cfg)
+    _check("moet_router_backward", lib().moet_router_backward(
+        ctypes.byref(c), _dev(logits, "logits"), _dev(topk_ids, "topk_ids"),
+        _dev(topk_gates, "topk_gates"), _dev(dy, "dy"), _dev(o, "o"), _dev(tok_row, "tok_row"),
+        _dev(token_mask, "token_mask"), _dev(seq_off, "seq_off"), int(n_seq),
+        _dev(counts, "counts"), _dev(seq_info, "seq_info"), _dev(lse, "lse"),
+        _dev(dloss, "dloss"), _dev(dgates, "dgates"), _dev(dlogits, "dlogits"),
+        _dev(status, "status"), _stream(stream)))
+
+
+def moet_block_norm(cfg, norm, h, y, gate, w_post, w_next, h_out, x, stream=None) -> None:
+    c = _cfg(cfg)
+    _check("moet_block_norm", lib().moet_block_norm(
+        ctypes.byref(c), ctypes.byref(norm), _dev(h, "h"), _dev(y, "y"), _dev(gate, "gate"),
+        _dev(w_post, "w_post"), _dev(w_next, "w_next"), _dev(h_out, "h_out"), _dev(x, "x"),
+        _stream(stream)))
+
+
+def moet_block_norm_backward(cfg, norm, h_out, y, gate, w_post, w_next, dh_out, dx, dh, dy,
+                             dgate, dw_post, dw_next, workspace, stream=None) -> None:
+    c = _cfg(cfg)
+    _check("moet_block_norm_backward", lib().moet_block_norm_backward(
+        ctypes.byref(c), ctypes.byref(norm), _dev(h_out, "h_out"), _dev(y, "y"),
+        _dev(gate, "gate"), _dev(w_post, "w_post"), _dev(w_next, "w_next"),
+        _dev(dh_out, "dh_out"), _dev(dx, "dx"), _dev(dh, "dh"), _dev(dy, "dy"),
+        _dev(dgate, "dgate"), _dev(dw_post, "dw_post"), _dev(dw_next, "dw_next"),
+        _dev(workspace, "workspace"), _stream(stream)))
+
+
+def moet_adamw_step(tensors, count, opt, lr, grad_scale, step, stream=None) -> None:
+    """`tensors`: a ctypes array of MoetAdamwTensor; `opt`: a MoetAdamw."""
+    _check("moet_adamw_step", lib().moet_adamw_step(
+        tensors, int(count), ctypes.byref(opt), _dev(lr, "lr"),
+        _dev(grad_scale, "grad_scale"), _dev(step, "step"), _stream(stream)))

@@ -1,0 +1,362 @@
+"""Training the block around the expert computation: the router's losses and gradient, the
+norms before and after the block, and the weights' AdamW step.  Each class owns its output
+buffers, as MoeLayer does, and calls the library's kernels (include/moeskew_train.h) on the
+current CUDA stream of its device, or on `stream`.  One object serves one stream at a time;
+its outputs are views that the next call overwrites.
+
+    norm = BlockNorm(wl, train=True)
+    router = RouterLoss(wl, n_seq=3)
+    opt = AdamW([w1, w2], lr=1e-3, state_bits=8)
+    layer = MoeLayer(wl, train=True, o_rows=True)
+
+    _, x = norm(h, w_next=w_in)                        # the norm before the block
+    y = layer(logits, x, w1, w2)
+    losses = router(logits, layer.view("topk_ids"), seq_off=seq_off)
+    h_out, _ = norm_out(h, y=y, w_post=w_out)          # behind it (an object of its own)
+    ...
+    g = norm_out.backward(h_out, y=y, w_post=w_out, dh_out=dh_out)
+    dx, dw1, dw2 = layer.backward(g.dy, w1, w2)
+    dlogits = layer.router_backward(router, logits, g.dy, dloss=dloss, seq_off=seq_off)
+    opt.step([dw1, dw2])
+"""
+from __future__ import annotations
+
+import collections
+import ctypes
+
+import torch
+
+from . import native as N
+
+_TYPES = {torch.float32: N.MOET_F32, torch.bfloat16: N.MOET_BF16,
+          torch.float8_e4m3fn: N.MOET_E4M3}
+
+
+def _device(device) -> torch.device:
+    dev = torch.device(device)
+    if dev.type != "cuda":
+        raise ValueError("the training operators run on a CUDA device")
+    return torch.device("cuda", torch.cuda.current_device()) if dev.index is None else dev
+
+
+def _need(t, name, dtype, n, dev, optional=False):
+    """Checks one array argument: a contiguous tensor of `dtype` on `dev` with `n` elements,
+    or a flat buffer of at least that many (what MoeLayer owns)."""
+    if t is None:
+        if optional:
+            return
+        raise TypeError(f"{name} is needed")
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise TypeError(f"{name} must be a tensor on {dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    have = t.numel()
+    if not t.is_contiguous() or (have != n and (have < n or t.dim() != 1)):
+        raise ValueError(f"{name} must be contiguous with {n} elements")
+
+
+class _OnDevice:
+    """Runs a call with the object's device current and the stream resolved on it."""
+
+    def _call(self, fn, *args, stream=None):
+        dev = self.device
+        if stream is None:
+            stream = torch.cuda.current_stream(dev).cuda_stream
+        elif isinstance(stream, torch.cuda.Stream):
+            if stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the arrays on {dev}")
+        if torch.cuda.current_device() == dev.index:
+            fn(*args, stream=stream)
+        else:
+            with torch.cuda.device(dev):
+                fn(*args, stream=stream)
+
+
+class RouterLoss(_OnDevice):
+    """Balance loss, z loss, per-expert counts and the gradient of the router's logits, for a
+    batch of `n_seq` packed sequences (moet_balance_loss, moet_router_backward)."""
+
+    def __init__(self, wl, n_seq: int = 1, device="cuda"):
+        self.cfg = wl if isinstance(wl, N.MoeCfg) else N.MoeCfg.of(wl)
+        self.n_seq = int(n_seq)
+        size = N.moet_workspace_size(self.cfg, self.n_seq, N.MOET_WS_BALANCE)
+        if size == 0:
+            raise ValueError("configuration or n_seq rejected by moet_workspace_size")
+        dev = self.device = _device(device)
+        T, E, k, S = self.cfg.T, self.cfg.E, self.cfg.k, self.n_seq
+        z = lambda *shape, dt=torch.float32: torch.zeros(shape, dtype=dt, device=dev)
+        self.losses = z(2)
+        self.counts = z(S, E, dt=torch.int32)
+        self.probs = z(S, E)
+        self.seq_info = z(S + 2, dt=torch.int32)
+        self._lse, self._dgates, self._dlogits = z(max(T, 1)), z(max(T * k, 1)), z(max(T * E, 1))
+        self.lse = self._lse[:T]
+        self.dgates = self._dgates[:T * k].view(T, k)
+        self.dlogits = self._dlogits[:T * E].view(T, E)
+        self.workspace = z(size, dt=torch.uint8)
+        self.status = z(4, dt=torch.int32)
+
+    def _check_batch(self, token_mask, seq_off):
+        _need(token_mask, "token_mask", torch.uint8, self.cfg.T, self.device, optional=True)
+        _need(seq_off, "seq_off", torch.int32, self.n_seq + 1, self.device,
+              optional=self.n_seq == 1)
+
+    def __call__(self, logits, topk_ids, token_mask=None, seq_off=None, stream=None):
+        """fp32 [2]: balance loss and z loss of logits fp32 [T, E] and the router's topk_ids
+        int32 [T, k].  token_mask uint8 [T] leaves tokens out; seq_off int32 [n_seq + 1] are
+        the sequences' bounds (None with one sequence: the whole batch)."""
+        c, dev = self.cfg, self.device
+        _need(logits, "logits", torch.float32, c.T * c.E, dev)
+        _need(topk_ids, "topk_ids", torch.int32, c.T * c.k, dev)
+        self._check_batch(token_mask, seq_off)
+        if c.T == 0:
+            logits, topk_ids, token_mask = self._dlogits, self._dlogits, None
+        self._call(N.moet_balance_loss, c, logits, topk_ids, token_mask, seq_off, self.n_seq,
+                   self.losses, self.counts, self.probs, self.seq_info, self._lse,
+                   self.workspace, self.status, stream=stream)
+        return self.losses
+
+    def backward(self, logits=None, topk_ids=None, topk_gates=None, dloss=None, dy=None, o=None,
+                 tok_row=None, token_mask=None, seq_off=None, stream=None):
+        """dlogits fp32 [T, E]: the losses' part with dloss (fp32 [2], their gradient; after
+        the forward call on the same logits, ids, mask and sequences), the gates' part with
+        dy (fp32 [T, d]), o (the expert output rows, bf16 [R_max, d]) and tok_row, or both.
+        The gates' gradient is in `dgates` then."""
+        c, dev = self.cfg, self.device
+        gates = dy is not None or o is not None or tok_row is not None
+        if not gates and dloss is None:
+            raise ValueError("nothing to take the gradient of: give dloss, or dy, o and tok_row")
+        if gates:
+            rows = N.moe_workspace_size(c, N.MOE_WS_ROWS)
+            _need(topk_ids, "topk_ids", torch.int32, c.T * c.k, dev)
+            _need(topk_gates, "topk_gates", torch.float32, c.T * c.k, dev)
+            _need(dy, "dy", torch.float32, c.T * c.d, dev)
+            _need(o, "o", torch.bfloat16, rows * c.d, dev)
+            _need(tok_row, "tok_row", torch.int32, c.T * c.k, dev)
+        if dloss is not None:
+            _need(dloss, "dloss", torch.float32, 2, dev)
+            _need(logits, "logits", torch.float32, c.T * c.E, dev)
+            self._check_batch(token_mask, seq_off)
+        if c.T == 0:
+            return self.dlogits
+        self._call(N.moet_router_backward, c, logits, topk_ids, topk_gates, dy, o, tok_row,
+                   token_mask, seq_off, self.n_seq, self.counts, self.seq_info, self._lse,
+                   dloss, self._dgates if gates else None, self._dlogits, self.status,
+                   stream=stream)
+        return self.dlogits
+
+    def clear_status(self):
+        self.status.zero_()
+
+    def read_status(self) -> int:
+        return int(self.status[0].item())
+
+
+BlockNormGrads = collections.namedtuple("BlockNormGrads", "dh dy dgate dw_post dw_next")
+
+
+class BlockNorm(_OnDevice):
+    """The norms before and after a block with the block's gate and residual scale, over T
+    rows of width d (moet_block_norm, moet_block_norm_backward):
+
+        h_out = res_scale h + out_scale gate norm(y; w_post),   x = bf16(norm(h_out; w_next))
+
+    `train` holds the backward's buffers too."""
+
+    def __init__(self, wl, h_dtype=torch.bfloat16, w_dtype=torch.float32, eps: float = 1e-6,
+                 w_offset: float = 0.0, res_scale: float = 1.0, out_scale: float = 1.0,
+                 train: bool = False, device="cuda"):
+        self.cfg = wl if isinstance(wl, N.MoeCfg) else N.MoeCfg.of(wl)
+        for t in (h_dtype, w_dtype):
+            if t not in (torch.float32, torch.bfloat16):
+                raise ValueError("h_dtype and w_dtype are torch.float32 or torch.bfloat16")
+        if not eps > 0:
+            raise ValueError("eps must be above 0")
+        size = N.moet_workspace_size(self.cfg, 1, N.MOET_WS_NORM_BWD)
+        if size == 0:
+            raise ValueError("configuration rejected by moet_workspace_size (d % 8 == 0 and "
+                             f"d <= {N.MOET_MAX_NORM_D} are needed)")
+        dev = self.device = _device(device)
+        T, d = self.cfg.T, self.cfg.d
+        self.h_dtype, self.w_dtype, self.train = h_dtype, w_dtype, bool(train)
+        self.norm = N.MoetNorm(eps, w_offset, res_scale, out_scale, _TYPES[h_dtype],
+                               _TYPES[w_dtype])
+        new = lambda dt, *shape: torch.zeros(shape, dtype=dt, device=dev)
+        rows = max(T, 1)
+        self.h_out, self.x = new(h_dtype, rows, d)[:T], new(torch.bfloat16, rows, d)[:T]
+        if train:
+            self.dh, self.dy = new(h_dtype, rows, d)[:T], new(torch.float32, rows, d)[:T]
+            self.dgate = new(torch.float32, rows)[:T]
+            self.dw_post, self.dw_next = new(torch.float32, d), new(torch.float32, d)
+            self.workspace = new(torch.uint8, size)
+
+    def _check(self, h, y, gate, w_post, w_next):
+        T, d, dev = self.cfg.T, self.cfg.d, self.device
+        _need(h, "h", self.h_dtype, T * d, dev)
+        _need(y, "y", torch.float32, T * d, dev, optional=True)
+        _need(gate, "gate", torch.float32, T, dev, optional=True)
+        _need(w_post, "w_post", self.w_dtype, d, dev, optional=True)
+        _need(w_next, "w_next", self.w_dtype, d, dev, optional=True)
+        if y is None and (gate is not None or w_post is not None):
+            raise ValueError("gate and w_post belong to y")
+
+    def __call__(self, h, y=None, gate=None, w_post=None, w_next=None, h_out=None, stream=None):
+        """(h_out, x): the residual stream behind the block and, with w_next, the next
+        block's bf16 rows.  Without y, h_out is h itself (a norm before the first block).
+        `h_out=` takes the result's place in the caller's buffer; it may be h itself."""
+        c = self.cfg
+        self._check(h, y, gate, w_post, w_next)
+        if y is None and w_next is None:
+            raise ValueError("nothing to compute: give y, w_next or both")
+        if y is None:
+            if h_out is not None:
+                raise ValueError("h_out is written only with y")
+        elif h_out is None:
+            h_out = self.h_out
+        else:
+            _need(h_out, "h_out", self.h_dtype, c.T * c.d, self.device)
+        x = None if w_next is None else self.x
+        if c.T:
+            self._call(N.moet_block_norm, c, self.norm, h, y, gate, w_post, w_next, h_out, x,
+                       stream=stream)
+        return (h if y is None else h_out), x
+
+    def backward(self, h_out, y=None, gate=None, w_post=None, w_next=None, dh_out=None, dx=None,
+                 stream=None) -> BlockNormGrads:
+        """The gradients of one forward call: `h_out` is the stream it returned, dh_out the
+        gradient of that, dx (fp32 [T, d]) of x; dh_out = None is 0.  Fields that belong to
+        an argument that is None are None."""
+        if not self.train:
+            raise ValueError("built without train=True")
+        c = self.cfg
+        T, d, dev = c.T, c.d, self.device
+        self._check(h_out, y, gate, w_post, w_next)
+        _need(dh_out, "dh_out", self.h_dtype, T * d, dev, optional=True)
+        _need(dx, "dx", torch.float32, T * d, dev, optional=True)
+        if (w_next is None) != (dx is None):
+            raise ValueError("dx and w_next are given together")
+        if dh_out is None and dx is None:
+            raise ValueError("give dh_out, dx or both")
+        only = lambda buf, arg: None if arg is None else buf
+        g = BlockNormGrads(self.dh, only(self.dy, y), only(self.dgate, gate),
+                           only(self.dw_post, w_post), only(self.dw_next, w_next))
+        if T:
+            self._call(N.moet_block_norm_backward, c, self.norm, h_out, y, gate, w_post, w_next,
+                       dh_out, dx, g.dh, g.dy, g.dgate, g.dw_post, g.dw_next, self.workspace,
+                       stream=stream)
+        else:
+            for dw in (g.dw_post, g.dw_next):
+                if dw is not None:
+                    dw.zero_()
+        return g
+
+
+class AdamW(_OnDevice):
+    """AdamW over `params` (fp32 or bf16 tensors on one device), updated in place
+    (moet_adamw_step).
+
+    `weight_decay`: one number, or one a tensor.  `state_bits`: 32 (fp32 moments) or 8 (e4m3
+    codes with an fp32 scale per 256 elements; `v` then holds the second moment's root).
+    `master`: True keeps fp32 masters of bf16 weights, made from the weights here; or a list
+    of them.  `m`, `v`, `m_scale`, `v_scale`: lists to take as states (a checkpoint's, or
+    views of a flat buffer); zeros by default.  `step`: steps that they have seen.
+
+    Steps taken and learning rate live on the device (`steps`, `lr`), so a captured step
+    replays with their current values: set_lr() between replays."""
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay=0.01, state_bits: int = 32, master=None, m=None, v=None,
+                 m_scale=None, v_scale=None, step: int = 0):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("no parameters")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits is 8 or 32")
+        if not all(0 <= b < 1 for b in betas) or not eps >= 0 or step < 0:
+            raise ValueError("betas in [0, 1), eps >= 0 and step >= 0 are needed")
+        first = self.params[0]
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise TypeError("params must be CUDA tensors")
+        dev = self.device = first.device
+        count = len(self.params)
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else \
+            [float(weight_decay)] * count
+        state = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+        sizes = [p.numel() for p in self.params]
+        blocks = [-(-n // N.MOET_ADAMW_BLOCK) for n in sizes]
+        if master is True:
+            master = [p.detach().float() if p.dtype is torch.bfloat16 else None
+                      for p in self.params]
+        zeros = lambda ns, dt: [torch.zeros(n, dtype=dt, device=dev) for n in ns]
+        self.m = zeros(sizes, state) if m is None else list(m)
+        self.v = zeros(sizes, state) if v is None else list(v)
+        self.m_scale = self.v_scale = None
+        if state_bits == 8:
+            self.m_scale = zeros(blocks, torch.float32) if m_scale is None else list(m_scale)
+            self.v_scale = zeros(blocks, torch.float32) if v_scale is None else list(v_scale)
+        elif m_scale is not None or v_scale is not None:
+            raise ValueError("scales belong to 8-bit states")
+        self.master = None if master is None else list(master)
+        for name, ts in (("weight_decay", decay), ("m", self.m), ("v", self.v),
+                         ("m_scale", self.m_scale), ("v_scale", self.v_scale),
+                         ("master", self.master)):
+            if ts is not None and len(ts) != count:
+                raise ValueError(f"{name}: {len(ts)} of them for {count} parameters")
+        spans = []
+        self._tensors = (N.MoetAdamwTensor * count)()
+        for i, p in enumerate(self.params):
+            if p.dtype not in (torch.float32, torch.bfloat16):
+                raise TypeError("params must be torch.float32 or torch.bfloat16")
+            _need(p, f"params[{i}]", p.dtype, sizes[i], dev)
+            own = [("m", self.m[i], state, sizes[i]), ("v", self.v[i], state, sizes[i])]
+            if state_bits == 8:
+                own += [("m_scale", self.m_scale[i], torch.float32, blocks[i]),
+                        ("v_scale", self.v_scale[i], torch.float32, blocks[i])]
+            w = None if self.master is None else self.master[i]
+            if w is not None:
+                if p.dtype is not torch.bfloat16:
+                    raise ValueError("fp32 weights have no master")
+                own.append(("master", w, torch.float32, sizes[i]))
+            for name, t, dt, n in own:
+                _need(t, f"{name}[{i}]", dt, n, dev)
+            for name, t, dt, n in own + [("params", p, p.dtype, sizes[i])]:
+                if n:
+                    spans.append((t.data_ptr(), t.data_ptr() + n * t.element_size(),
+                                  f"{name}[{i}]"))
+            e = self._tensors[i]
+            e.p, e.m, e.v = p.data_ptr(), self.m[i].data_ptr(), self.v[i].data_ptr()
+            if state_bits == 8:
+                e.m_scale, e.v_scale = self.m_scale[i].data_ptr(), self.v_scale[i].data_ptr()
+            e.master = None if w is None else w.data_ptr()
+            e.n, e.weight_decay = sizes[i], decay[i]
+            e.p_dtype, e.state_dtype = _TYPES[p.dtype], _TYPES[state]
+        spans.sort()
+        for (_, end, a), (begin, _, b) in zip(spans, spans[1:]):
+            if begin < end:
+                raise ValueError(f"{a} and {b} share memory")
+        self._sizes = sizes
+        self._opt = N.MoetAdamw(float(betas[0]), float(betas[1]), float(eps))
+        self.lr = torch.full((4,), float(lr), device=dev)
+        self.steps = torch.tensor([step, 0, 0, 0], dtype=torch.int32, device=dev)
+
+    def set_lr(self, lr: float) -> None:
+        """Sets the learning rate of the steps that follow on the current stream."""
+        self.lr.fill_(float(lr))
+
+    def step(self, grads, grad_scale=None, stream=None) -> None:
+        """One step with `grads` (fp32 or bf16, one a parameter, of its size).  `grad_scale`:
+        fp32 device tensor that multiplies them (a clip or a loss scale's inverse); when it
+        is not finite, the step is left out."""
+        grads = list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
+        dev = self.device
+        for i, (e, g, n) in enumerate(zip(self._tensors, grads, self._sizes)):
+            t = _TYPES.get(g.dtype) if isinstance(g, torch.Tensor) else None
+            if t is None or t == N.MOET_E4M3:
+                raise TypeError(f"grads[{i}] must be a torch.float32 or torch.bfloat16 tensor")
+            _need(g, f"grads[{i}]", g.dtype, n, dev)
+            e.g, e.g_dtype = g.data_ptr(), t
+        _need(grad_scale, "grad_scale", torch.float32, 1, dev, optional=True)
+        self._call(N.moet_adamw_step, self._tensors, len(grads), self._opt, self.lr, grad_scale,
+                   self.steps, stream=stream)

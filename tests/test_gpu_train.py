@@ -1,0 +1,750 @@
+"""GPU parity of the training operators (moeskew_train.h) against their 64-bit forms, through
+the package's classes and the C ABI.
+
+Tolerances, with u = 2^-24 (half a step of fp32): a sum of n fp32 terms in the kernels' order
+(a thread's run of at most s terms, then log2 steps over lanes and warps) is off by at most
+(s + 12) u times the sum of the terms' sizes, expf by 2 steps plus the rounding of its
+argument, a root or a quotient by 2 steps.  Each check states the multiple of u it takes times
+the sizes that enter (`size`, computed in 64 bits with absolute values, so that cancellation
+is counted), plus half a step of the type that is stored: 2^-8 of the value for bf16, 2^-4 for
+e4m3 (half its smallest step, 2^-10 of the scale, below the normal numbers)."""
+import numpy as np
+import pytest
+import torch
+
+import train_oracle as R
+from skew_aware_token_b200 import native as N
+from skew_aware_token_b200.synth import WORKLOADS, Workload
+from skew_aware_token_b200.train import AdamW, BlockNorm, RouterLoss
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BF16 = 2.0 ** -8
+DEV = "cuda"
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def close(got, want, tol, what):
+    """|got - want| <= tol per element, all in 64 bits on the host."""
+    got, want = got.detach().double().cpu(), want.detach().double().cpu()
+    assert got.shape == want.shape, what
+    assert bool(torch.isfinite(got).all()), f"{what}: not finite"
+    over = (got - want).abs() - torch.as_tensor(tol, dtype=torch.float64)
+    assert bool((over <= 0).all()), f"{what}: over its bound by {float(over.max()):.3e}"
+
+
+def workload(T, d=256, E=8, k=2, beta=64):
+    return Workload("case", T=T, d=d, E=E, k=k, f=128, beta=beta, P=1, s=0)
+
+
+# ------------------------------------------------------------------------- router losses
+def router_inputs(T, E, k, seed=0):
+    logits = torch.randn(T, E, generator=gen(seed)) * 2 - torch.arange(1, E + 1).log()
+    top, ids = logits.topk(k, dim=1)
+    return logits, ids.int().contiguous(), torch.softmax(top, 1).contiguous()
+
+
+LOSS_CASES = [
+    # T, E, k, seq_off, mask: "none" | "some" | "all" masked
+    (1, 1, 1, None, "none"), (1, 256, 8, None, "none"), (7, 33, 3, [0, 0, 7, 7], "some"),
+    (256, 8, 2, None, "some"), (1111, 12, 4, [5, 300, 301, 900, 1000], "some"),
+    (515, 60, 6, [0, 515], "none"), (640, 128, 8, list(range(0, 641, 5)), "some"),
+    (100, 256, 8, list(range(101)), "none"), (2048, 64, 8, [0, 31, 33, 64, 2048], "some"),
+    (300, 200, 5, [0, 100, 200, 300], "all"), (33, 96, 2, [33, 33], "none"),
+]
+
+
+@pytest.mark.parametrize("T,E,k,off,masked", LOSS_CASES)
+def test_router_losses(T, E, k, off, masked):
+    logits, ids, _ = router_inputs(T, E, k)
+    mask = None if masked == "none" else (torch.rand(T, generator=gen(1)) > 0.3).to(torch.uint8)
+    if masked == "all":
+        mask.zero_()
+    elif mask is not None and off is not None and len(off) > 3:
+        mask[off[1]:off[2]] = 0                       # a sequence that its mask leaves empty
+    on = torch.zeros(T, dtype=torch.bool)
+    for a, b in R.spans(T, off):
+        on[a:b] = True
+    if mask is not None:
+        on &= mask.bool()
+    dirty = logits.clone()
+    dirty[~on] = float("nan")                          # nothing of a row that does not count
+    dirty_ids = ids.clone()
+    dirty_ids[~on] = 1 << 30
+    S = 1 if off is None else len(off) - 1
+    r = RouterLoss(workload(T, E=E, k=k), n_seq=S, device=DEV)
+    r.workspace.fill_(255)
+    for buf in (r.losses, r.probs, r._lse):
+        buf.fill_(float("nan"))
+    dev = lambda t, dt=None: None if t is None else torch.as_tensor(t, dtype=dt).to(DEV)
+    args = (dev(dirty), dev(dirty_ids), dev(mask), dev(off, torch.int32))
+    r(*args)
+    torch.cuda.synchronize()
+    assert r.read_status() == 0, N.moe_status_string(r.read_status())
+    b, z, c, p, lse = R.router_losses(logits, ids, mask, off)
+    assert torch.equal(r.counts.cpu().double(), c)
+    n_s = [int(on[a:e].sum()) for a, e in R.spans(T, off)]
+    assert r.seq_info.tolist() == n_s + [sum(n_s), sum(n > 0 for n in n_s)]
+    # |x - top| < 32 here: exp's argument is off by 32 u, a row's sum of at most 8 + 5 steps
+    close(r.lse, lse, 64 * U * (1 + lse.abs()), "lse")
+    close(r.probs, p, 256 * U * p, "probs")
+    close(r.losses, torch.stack([b, z]), 256 * U * (1 + torch.stack([b, z])), "losses")
+    first = [t.clone() for t in (r.losses, r.counts, r.probs, r.lse)]
+    r(*args)
+    assert all(torch.equal(a, t) for a, t in zip(first, (r.losses, r.counts, r.probs, r.lse)))
+
+
+def test_router_losses_lowest_values():
+    """Experts masked with the type's lowest value are finite logits of no probability."""
+    low = torch.finfo(torch.float32).min
+    logits = torch.zeros(64, 16)
+    logits[:, 4:] = low
+    ids = torch.tensor([[0, 1]]).repeat(64, 1).int()
+    r = RouterLoss(workload(64, E=16, k=2), device=DEV)
+    r(logits.to(DEV), ids.to(DEV))
+    d = r.backward(logits.to(DEV), dloss=torch.ones(2, device=DEV))
+    assert r.read_status() == 0
+    want = torch.tensor([0.25] * 4 + [0.0] * 12)
+    close(r.probs[0], want, 8 * U, "probs")
+    assert bool((d[:, 4:] == 0).all()) and bool(torch.isfinite(d).all())
+    # a row of lowest values alone is a uniform row, its z loss the square's overflow
+    r(torch.full((64, 16), low, device=DEV), ids.to(DEV))
+    close(r.probs[0], torch.full((16,), 1 / 16), 8 * U, "probs")
+    assert float(r.losses[1]) == float("inf") and bool(torch.isfinite(r.lse).all())
+
+
+def test_router_losses_status():
+    logits, ids, _ = router_inputs(40, 8, 2)
+    for value in (float("nan"), float("inf"), float("-inf")):
+        bad = logits.clone()
+        bad[17, 3] = value
+        r = RouterLoss(workload(40), device=DEV)
+        r(bad.to(DEV), ids.to(DEV))
+        assert r.read_status() == N.MOE_STATUS_NONFINITE
+    for value in (-1, 8, 1 << 30):
+        bad = ids.clone()
+        bad[3, 1] = value
+        r = RouterLoss(workload(40), device=DEV)
+        r(logits.to(DEV), bad.to(DEV))
+        assert r.read_status() == N.MOE_STATUS_BAD_ID
+        assert int(r.counts.sum()) == 79
+    for off in ([0, 20, 10, 40], [-1, 10, 20, 40], [0, 10, 20, 41], [0, 1 << 30, 5, 40]):
+        r = RouterLoss(workload(40), n_seq=3, device=DEV)
+        r(logits.to(DEV), ids.to(DEV), None, torch.tensor(off, dtype=torch.int32, device=DEV))
+        assert r.read_status() & N.MOET_STATUS_BAD_SEQ, off
+    r = RouterLoss(workload(0), device=DEV)                # no tokens
+    assert r(torch.zeros(0, 8, device=DEV), torch.zeros(0, 2, dtype=torch.int32, device=DEV)
+             ).tolist() == [0, 0]
+    assert r.read_status() == 0 and r.seq_info.tolist() == [0, 0, 0]
+
+
+# ----------------------------------------------------------------------- router gradient
+def rows_of(ids, E, beta):
+    """tok_row of the block-aligned, expert-major rows, by a loop."""
+    T, k = ids.shape
+    counts = torch.bincount(ids.reshape(-1).long(), minlength=E)
+    blocks = (counts + beta - 1) // beta
+    base = (beta * (blocks.cumsum(0) - blocks)).tolist()
+    out = torch.empty(T, k, dtype=torch.int32)
+    for t in range(T):
+        for j in range(k):
+            e = int(ids[t, j])
+            out[t, j] = base[e]
+            base[e] += 1
+    return out
+
+
+GRAD_CASES = [
+    # T, d, E, k, seq_off, masked
+    (1, 8, 1, 1, None, False), (1, 7168, 256, 8, None, False), (33, 520, 33, 3, [0, 9, 33], True),
+    (257, 512, 12, 4, [3, 3, 100, 250], True), (70, 2056, 200, 8, None, False),
+    (300, 64, 128, 6, [0, 150, 300], True), (5, 8192, 2, 2, None, True),
+]
+
+
+@pytest.mark.parametrize("T,d,E,k,off,masked", GRAD_CASES)
+def test_router_gradient(T, d, E, k, off, masked):
+    wl = workload(T, d=d, E=E, k=k)
+    logits, ids, gates = router_inputs(T, E, k, seed=2)
+    mask = (torch.rand(T, generator=gen(3)) > 0.3).to(torch.uint8) if masked else None
+    R_max = N.moe_workspace_size(wl, N.MOE_WS_ROWS)
+    tok_row = rows_of(ids, E, wl.beta)
+    o = torch.randn(R_max, d, generator=gen(4)).bfloat16()
+    dy = torch.randn(T, d, generator=gen(5))
+    dloss = torch.tensor([3.0, -0.5])
+    # the formula by autograd: gates are the softmax over the chosen logits
+    x = logits.double().requires_grad_()
+    b, z = R.router_losses(x, ids, mask, off)[:2]
+    rows = o.double()[tok_row.long()]
+    dg = torch.einsum("tkd,td->tk", rows, dy.double())
+    g = torch.softmax(x.gather(1, ids.long()), 1)
+    loss_part, = torch.autograd.grad(3.0 * b - 0.5 * z, x, allow_unused=True)
+    gate_part, = torch.autograd.grad((g * dg).sum(), x)
+    loss_part = torch.zeros_like(gate_part) if loss_part is None else loss_part
+    S = 1 if off is None else len(off) - 1
+    r = RouterLoss(wl, n_seq=S, device=DEV)
+    off_d = None if off is None else torch.tensor(off, dtype=torch.int32, device=DEV)
+    mask_d = None if mask is None else mask.to(DEV)
+    L, I, G = logits.to(DEV), ids.to(DEV), gates.to(DEV)
+    r(L, I, mask_d, off_d)
+    run = lambda **kw: r.backward(L, I, G, token_mask=mask_d, seq_off=off_d, **kw).clone()
+    via = dict(dy=dy.to(DEV), o=o.to(DEV), tok_row=tok_row.to(DEV))
+    r._dlogits.fill_(float("nan"))
+    r._dgates.fill_(float("nan"))
+    both = run(dloss=dloss.to(DEV), **via)
+    # dgates: at most 8 * 4 terms a thread (d <= 8192 over 256 threads), 8 more steps
+    size = torch.einsum("tkd,td->tk", rows.abs(), dy.double().abs())
+    close(r.dgates, dg, 64 * U * size, "dgates")
+    gd = g.detach()
+    gate_size = torch.zeros_like(x).scatter_add_(
+        1, ids.long(), gd * (size + (gd * size).sum(1, keepdim=True))).detach()
+    p = torch.softmax(logits.double(), 1)
+    # a_se by its parts: |dL/dp| is at most its largest, p is off by (64 + 32) u
+    with torch.no_grad():
+        _, _, c, _, lse = R.router_losses(logits, ids, mask, off)
+        n_s = torch.tensor([float(sum(1 for t in range(a, e) if mask is None or mask[t]))
+                            for a, e in R.spans(T, off)]).double()
+        seqs, n = max(1, int((n_s > 0).sum())), max(1.0, float(n_s.sum()))
+        a_max = (3.0 * E * c / (seqs * k * n_s.clamp(min=1)[:, None] ** 2)).max()
+        loss_size = p * (2 * a_max + (lse / n).abs()[:, None])
+    close(run(dloss=dloss.to(DEV)), loss_part, 256 * U * loss_size, "losses' part")
+    close(run(**via), gate_part, 128 * U * gate_size, "gates' part")
+    close(both, loss_part + gate_part, 256 * U * loss_size + 128 * U * gate_size, "both")
+    assert torch.equal(both, run(dloss=dloss.to(DEV), **via))
+    assert r.read_status() == 0
+
+
+def test_router_gradient_bad_rows_and_repeats():
+    T, d, E, k = 20, 64, 8, 3
+    wl = workload(T, d=d, E=E, k=k)
+    R_max = N.moe_workspace_size(wl, N.MOE_WS_ROWS)
+    logits, ids, gates = router_inputs(T, E, k, seed=6)
+    o = torch.randn(R_max, d, generator=gen(7)).bfloat16()
+    dy = torch.randn(T, d, generator=gen(8))
+    tok_row = torch.randint(0, R_max, (T, k), generator=gen(9)).int()   # rows shared by tokens
+    ids[4] = 5                                                        # one expert k times
+    r = RouterLoss(wl, device=DEV)
+    go = lambda i, t: r.backward(topk_ids=i.to(DEV), topk_gates=gates.to(DEV), dy=dy.to(DEV),
+                                 o=o.to(DEV), tok_row=t.to(DEV)).cpu()
+    got = go(ids, tok_row)
+    dg = torch.einsum("tkd,td->tk", o.double()[tok_row.long()], dy.double())
+    part = gates.double() * (dg - (gates.double() * dg).sum(1, keepdim=True))
+    close(got, torch.zeros(T, E, dtype=torch.float64).scatter_add_(1, ids.long(), part),
+          64 * U * float(dg.abs().max() + 50), "repeats")
+    assert r.read_status() == 0
+    for bad_row in (-1, R_max, 1 << 30):
+        r.clear_status()
+        t = tok_row.clone()
+        t[7, 2] = bad_row
+        assert torch.isfinite(go(ids, t)).all() and r.read_status() == N.MOE_STATUS_BAD_ID
+        assert float(r.dgates[7, 2]) == 0
+    for bad_id in (-1, E, 1 << 30):
+        r.clear_status()
+        i = ids.clone()
+        i[7, 2] = bad_id
+        assert torch.isfinite(go(i, tok_row)).all() and r.read_status() == N.MOE_STATUS_BAD_ID
+
+
+# ---------------------------------------------------------------------------- block norms
+NORM_SHAPES = [(1, 8), (1, 7168), (3, 8192), (5, 264), (130, 512), (301, 1000), (64, 2048),
+               (700, 136), (40, 4104)]
+TYPES = [(torch.bfloat16, torch.float32), (torch.float32, torch.float32),
+         (torch.bfloat16, torch.bfloat16), (torch.float32, torch.bfloat16)]
+PARTS = ["all", "no_gate", "no_post", "no_next", "first"]
+
+
+def norm_inputs(T, d, ht, wt, parts, seed=0):
+    mk = lambda *s, n: torch.randn(*s, generator=gen(seed + n))
+    a = dict(h=mk(T, d, n=1).to(ht), y=mk(T, d, n=2) * 0.5, gate=torch.rand(T, generator=gen(3)),
+             w_post=(1 + 0.2 * mk(d, n=4)).to(wt), w_next=(1 + 0.2 * mk(d, n=5)).to(wt))
+    drop = dict(all=(), no_gate=("gate",), no_post=("w_post",), no_next=("w_next",),
+                first=("y", "gate", "w_post"))[parts]
+    return {n: None if n in drop else t for n, t in a.items()}
+
+
+def on_gpu(a):
+    return {n: None if t is None else t.to(DEV) for n, t in a.items()}
+
+
+def wide(a):
+    return {n: None if t is None else t.double() for n, t in a.items()}
+
+
+CONST = dict(eps=1e-5, w_offset=0.25, res_scale=0.8, out_scale=-0.6)
+
+
+@pytest.mark.parametrize("parts", PARTS)
+@pytest.mark.parametrize("T,d", NORM_SHAPES)
+@pytest.mark.parametrize("ht,wt", TYPES, ids=lambda t: str(t)[6:])
+def test_block_norm(T, d, ht, wt, parts):
+    a = norm_inputs(T, d, ht, wt, parts)
+    norm = BlockNorm(workload(T, d=d), h_dtype=ht, w_dtype=wt, device=DEV, **CONST)
+    for buf in (norm.h_out, norm.x):
+        buf.fill_(float("nan"))
+    h_out, x = norm(**on_gpu(a))
+    q = wide(a)
+    want_h, want_x = R.block_norm(q["h"], q["y"], q["gate"], q["w_post"], q["w_next"], **CONST)
+    store = BF16 if ht is torch.bfloat16 else 0.0
+    # a mean's sum: 16 terms a thread and 10 steps; the root halves it; a few products more
+    size = want_h.abs() if a["y"] is None else \
+        (CONST["res_scale"] * q["h"]).abs() + (want_h - CONST["res_scale"] * q["h"]).abs()
+    if a["y"] is not None:
+        close(h_out, want_h, store * want_h.abs() + 32 * U * size, "h_out")
+    else:
+        assert h_out.data_ptr() != norm.h_out.data_ptr() and torch.equal(h_out.cpu(), a["h"])
+    if x is None:
+        assert a["w_next"] is None
+        return
+    r = 1 / torch.sqrt((want_h ** 2).mean(1, keepdim=True) + CONST["eps"])
+    x_size = want_x.abs() + size * r * (q["w_next"] + CONST["w_offset"]).abs()
+    close(x, want_x, BF16 * want_x.abs() + 64 * U * x_size, "x")
+
+
+def test_block_norm_in_place_and_zero_rows():
+    a = on_gpu(norm_inputs(50, 1024, torch.float32, torch.float32, "all"))
+    norm = BlockNorm(workload(50, d=1024), h_dtype=torch.float32, device=DEV, **CONST)
+    h_out, x = (t.clone() for t in norm(**a))
+    got, x2 = norm(**a, h_out=a["h"])
+    assert got.data_ptr() == a["h"].data_ptr()
+    assert torch.equal(got, h_out) and torch.equal(x2, x)
+    z = dict(h=torch.zeros(50, 1024, device=DEV), y=torch.zeros(50, 1024, device=DEV),
+             w_post=a["w_post"], w_next=a["w_next"])
+    h_out, x = norm(**z)
+    assert float(h_out.abs().max()) == 0 and float(x.float().abs().max()) == 0
+    # a row's values stay its own: an infinite or NaN row leaves the others' bits alone
+    b = on_gpu(norm_inputs(50, 1024, torch.float32, torch.float32, "all"))
+    clean = [t.clone() for t in norm(**b)]
+    b["y"][13] = float("nan")
+    b["h"][20, 5] = float("inf")
+    rest = [i for i in range(50) if i not in (13, 20)]
+    for got, want in zip(norm(**b), clean):
+        assert torch.equal(got[rest], want[rest]) and bool(torch.isnan(got[13]).all())
+
+
+@pytest.mark.parametrize("parts", PARTS)
+@pytest.mark.parametrize("T,d", NORM_SHAPES)
+@pytest.mark.parametrize("ht,wt", TYPES, ids=lambda t: str(t)[6:])
+def test_block_norm_gradient(T, d, ht, wt, parts):
+    a = norm_inputs(T, d, ht, wt, parts, seed=10)
+    norm = BlockNorm(workload(T, d=d), h_dtype=ht, w_dtype=wt, train=True, device=DEV, **CONST)
+    dh_out = torch.randn(T, d, generator=gen(20)).to(ht)
+    dx = None if a["w_next"] is None else torch.randn(T, d, generator=gen(21))
+    for buf in (norm.dh, norm.dy, norm.dgate, norm.dw_post, norm.dw_next):
+        buf.fill_(float("nan"))
+    norm.workspace.fill_(255)
+    # the stream behind the block is what is stored: any row may stand for it
+    b = on_gpu(a)
+    run = lambda: norm.backward(b["h"], y=b["y"], gate=b["gate"], w_post=b["w_post"],
+                                w_next=b["w_next"], dh_out=dh_out.to(DEV),
+                                dx=None if dx is None else dx.to(DEV))
+    g = run()
+    # autograd of the two halves at the stored stream
+    q = wide(a)
+    leaf = {n: t.clone().requires_grad_() for n, t in q.items() if t is not None}
+    h = leaf["h"]
+    u = dh_out.double()
+    zero = torch.zeros(())
+    M = u.abs()
+    if dx is not None:
+        x = R.rms_norm(h, leaf["w_next"], CONST["eps"], CONST["w_offset"])
+        gh, gw = torch.autograd.grad((x * dx.double()).sum(), (h, leaf["w_next"]))
+        u = u + gh
+        wn = (q["w_next"] + CONST["w_offset"]).abs()
+        A = 1 / torch.sqrt((q["h"] ** 2).mean(1, keepdim=True) + CONST["eps"])
+        dxa = dx.double().abs()
+        M = M + A * dxa * wn + A ** 3 * q["h"].abs() * (dxa * wn * q["h"].abs()).mean(1, keepdim=True)
+        # the weights' sums: at most 700 rows over 148 CTAs' groups, then 74 + 8 partial rows
+        close(g.dw_next, gw, 160 * U * (dxa * A * q["h"].abs()).sum(0), "dw_next")
+    store = BF16 if ht is torch.bfloat16 else 0.0
+    res = CONST["res_scale"] if a["y"] is not None else 1.0
+    close(g.dh, res * u, store * (res * u).abs() + 64 * U * M, "dh")
+    if a["y"] is None:
+        assert g.dy is None and g.dgate is None and g.dw_post is None
+    else:
+        names = [n for n in ("y", "gate", "w_post") if n in leaf]
+        out, _ = R.block_norm(torch.zeros_like(q["h"]), leaf["y"], leaf.get("gate"),
+                              leaf.get("w_post"), None, **CONST)
+        grads = dict(zip(names, torch.autograd.grad((out * u).sum(), [leaf[n] for n in names])))
+        y = q["y"].abs()
+        ry, wp = torch.ones(T, 1).double(), torch.ones(d).double()
+        if a["w_post"] is not None:
+            ry = 1 / torch.sqrt((q["y"] ** 2).mean(1, keepdim=True) + CONST["eps"])
+            wp = (q["w_post"] + CONST["w_offset"]).abs()
+        gt = torch.ones(T, 1).double() if a["gate"] is None else q["gate"][:, None]
+        c = abs(CONST["out_scale"])
+        size = c * gt * ry * M * wp
+        if a["w_post"] is not None:
+            size = size + c * gt * ry ** 3 * y * (M * wp * y).mean(1, keepdim=True)
+            close(g.dw_post, grads["w_post"], 160 * U * (c * gt * ry * M * y).sum(0), "dw_post")
+        close(g.dy, grads["y"], 96 * U * size, "dy")
+        if a["gate"] is not None:
+            close(g.dgate, grads["gate"], 96 * U * (c * ry * M * wp * y).sum(1), "dgate")
+    for name, arg in (("dgate", "gate"), ("dw_post", "w_post"), ("dw_next", "w_next")):
+        assert (getattr(g, name) is None) == (a[arg] is None)
+    first = [None if t is None else t.clone() for t in g]
+    assert all(t is None or torch.equal(t, f) for t, f in zip(run(), first))
+
+
+def test_block_norm_gradient_parts_and_in_place():
+    """dh_out = None is zeros; dh may take dh_out's place (C ABI)."""
+    T, d = 77, 768
+    a = on_gpu(norm_inputs(T, d, torch.float32, torch.float32, "all", seed=30))
+    norm = BlockNorm(workload(T, d=d), h_dtype=torch.float32, train=True, device=DEV, **CONST)
+    dx = torch.randn(T, d, generator=gen(31)).to(DEV)
+    kw = dict(y=a["y"], gate=a["gate"], w_post=a["w_post"], w_next=a["w_next"], dx=dx)
+    zero = [t.clone() for t in norm.backward(a["h"], dh_out=torch.zeros(T, d, device=DEV), **kw)]
+    assert all(torch.equal(t, z) for t, z in zip(norm.backward(a["h"], **kw), zero))
+    dh = torch.randn(T, d, generator=gen(32)).to(DEV)
+    want = [t.clone() for t in norm.backward(a["h"], dh_out=dh, **kw)]
+    N.moet_block_norm_backward(norm.cfg, norm.norm, a["h"], a["y"], a["gate"], a["w_post"],
+                               a["w_next"], dh, dx, dh, norm.dy, norm.dgate, norm.dw_post,
+                               norm.dw_next, norm.workspace)
+    assert torch.equal(dh, want[0])
+    empty = BlockNorm(workload(0, d=d), train=True, device=DEV)
+    none = torch.zeros(0, d, device=DEV)
+    empty.dw_next.fill_(7)
+    g = empty.backward(none.bfloat16(), w_next=a["w_next"], dx=none)
+    assert float(g.dw_next.abs().max()) == 0
+    # through the C ABI too: no rows, weight gradients of zero
+    empty.dw_next.fill_(7)
+    N.moet_block_norm_backward(empty.cfg, empty.norm, a["h"], None, None, None, a["w_next"], dh,
+                               dx, dh, None, None, None, empty.dw_next, empty.workspace)
+    assert float(empty.dw_next.abs().max()) == 0
+
+
+# --------------------------------------------------------------------------------- AdamW
+SIZES = [1, 3, 255, 256, 257, 2048, 2049, 5000, 0, 70001]
+KINDS = [(torch.float32, False), (torch.bfloat16, False), (torch.bfloat16, True)]
+B1, B2, EPS, LR = 0.9, 0.95, 1e-8, 3e-3
+
+
+def adam_inputs(sizes, pt, gt, seed=0):
+    ps = [torch.randn(n, generator=gen(seed + i)).to(pt) for i, n in enumerate(sizes)]
+    gs = [(torch.randn(n, generator=gen(seed + 100 + i)) * 0.1 ** (i % 5)).to(gt)
+          for i, n in enumerate(sizes)]
+    return ps, gs
+
+
+@pytest.mark.parametrize("gt", [torch.float32, torch.bfloat16], ids=["g32", "g16"])
+@pytest.mark.parametrize("pt,master", KINDS, ids=["f32", "bf16", "master"])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw(bits, pt, master, gt):
+    ps, gs = adam_inputs(SIZES, pt, gt)
+    decay = [0.1 * (i % 3) for i in range(len(SIZES))]
+    opt = AdamW([p.to(DEV) for p in ps], lr=LR, betas=(B1, B2), eps=EPS, weight_decay=decay,
+                state_bits=bits, master=True if master else None)
+    host = lambda ts: [t.cpu() for t in ts]
+    for step in range(1, 4):
+        gd = [(g.float() * step).to(gt) for g in gs]
+        before = {n: host(getattr(opt, n)) for n in ("params", "m", "v")}
+        if bits == 8:
+            before["m"] = [R.of_8bit(c, s) for c, s in zip(before["m"], host(opt.m_scale))]
+            before["v"] = [R.of_8bit(c, s) ** 2 for c, s in zip(before["v"], host(opt.v_scale))]
+        w = host(opt.master) if master else before["params"]
+        opt.step([g.to(DEV) for g in gd])
+        assert opt.steps.tolist()[:2] == [step, 0]
+        for i, n in enumerate(SIZES):
+            if n == 0:
+                continue
+            g, m0, v0 = gd[i].double(), before["m"][i].double(), before["v"][i].double()
+            p, m, v = R.adamw(w[i].double(), g, m0, v0, step, LR, B1, B2, EPS, decay[i])
+            ms = (B1 * m0).abs() + ((1 - B1) * g).abs()
+            # the moment behind a cancelled sum reaches the step too
+            up = ms / (1 - B1 ** step) / ((v / (1 - B2 ** step)).sqrt() + EPS)
+            tol = U * (8 * p.abs() + 8 * w[i].double().abs() + 48 * LR * up)
+            new = opt.params[i]
+            if master:
+                close(opt.master[i], p, tol, "master")
+                assert torch.equal(opt.master[i].bfloat16(), new)
+            close(new, p, tol + (BF16 * p.abs() if pt is torch.bfloat16 else 0), f"p[{i}]")
+            if bits == 32:
+                close(opt.m[i], m, 4 * U * ms, "m")
+                close(opt.v[i], v, 6 * U * v, "v")
+                continue
+            # the stored form is defined by its fp32 roundings: the same bits
+            f = lambda t: torch.tensor(t, dtype=torch.float32)
+            g32 = gd[i].float()
+            m32 = before["m"][i] * f(B1) + g32 * f(1 - B1)
+            v32 = before["v"][i] * f(B2) + (g32 * f(1 - B2)) * g32
+            # (torch's fp32 root on the CPU is up to a step off; the 64-bit one, rounded, is the
+            # nearest fp32 value, since 53 >= 2 * 24 + 2 bits)
+            r32 = v32.double().sqrt().float()
+            for got, s, (want, ws) in ((opt.m[i], opt.m_scale[i], R.to_8bit(m32, False)),
+                                       (opt.v[i], opt.v_scale[i], R.to_8bit(r32, True))):
+                assert torch.equal(s.cpu(), ws)
+                assert torch.equal(got.cpu().view(torch.uint8), want.view(torch.uint8))
+            # and within half a step of e4m3 of the 64-bit moments
+            sc = opt.m_scale[i].cpu().double().repeat_interleave(256)[:n]
+            close(R.of_8bit(opt.m[i].cpu(), opt.m_scale[i].cpu()), m,
+                  2.0 ** -4 * m.abs() + 2.0 ** -10 * sc + 16 * U * ms, "m")
+            sc = opt.v_scale[i].cpu().double().repeat_interleave(256)[:n]
+            close(R.of_8bit(opt.v[i].cpu(), opt.v_scale[i].cpu()), v.sqrt(),
+                  (2.0 ** -4 + 16 * U) * v.sqrt() + 2.0 ** -9 * sc, "root of v")
+
+
+def test_adamw_scale_skip_and_mixed_tensors():
+    """grad_scale multiplies; a scale that is not finite leaves the step out; tensors of every
+    kind and more of them than one launch holds step together."""
+    kinds = [(pt, gt, m) for pt, m in KINDS for gt in (torch.float32, torch.bfloat16)]
+    ps, gs, ms = [], [], []
+    for i in range(900):
+        pt, gt, m = kinds[i % 6] if i < 60 else kinds[0]
+        p, g = adam_inputs([1 + 37 * i % 400], pt, gt, seed=i)
+        ps += [p[0].to(DEV)]
+        gs += [g[0].to(DEV)]
+        ms += [p[0].float().to(DEV) if m else None]
+    p0 = [p.clone() for p in ps]
+    opt = AdamW(ps, lr=LR, betas=(B1, B2), weight_decay=0.1, master=ms)
+    for bad in (float("nan"), float("inf")):
+        opt.step(gs, grad_scale=torch.tensor([bad], device=DEV))
+        assert opt.steps.tolist()[:2] == [0, 0]
+        assert all(torch.equal(a, b) for a, b in zip(ps, p0))
+        assert all(float(m.abs().max()) == 0 for m in opt.m)
+    opt.step(gs, grad_scale=torch.tensor([0.5], device=DEV))
+    assert opt.steps.tolist()[:2] == [1, 0]
+    for i, (p, q, g) in enumerate(zip(ps, p0, gs)):
+        q, g = q.double().cpu(), 0.5 * g.double().cpu()
+        want, m, _ = R.adamw(q, g, 0 * g, 0 * g, 1, LR, B1, B2, EPS, 0.1)
+        close(opt.m[i], m, 4 * U * m.abs(), "m")
+        close(p, want, U * (16 * q.abs() + 64 * LR) + (BF16 * want.abs() if p.dtype is torch.bfloat16
+                                                       else 0), f"p[{i}]")
+
+
+def test_adamw_bad_gradients_stay_in_their_block():
+    n = 1024
+    for bits in (32, 8):
+        p = torch.ones(n, device=DEV)
+        opt = AdamW([p], lr=LR, state_bits=bits)
+        g = torch.randn(n, generator=gen(0)).to(DEV)
+        g[300], g[301] = float("nan"), float("inf")
+        opt.step([g])
+        assert not bool(torch.isfinite(p[300:302]).any())
+        rest = torch.ones(n, dtype=torch.bool)
+        rest[300:302] = False
+        assert bool(torch.isfinite(p.cpu()[rest]).all())
+        if bits == 8:
+            ok = torch.isfinite(opt.m_scale[0]).cpu().tolist()
+            assert ok == [True, False, True, True]
+    # blocks of nothing, and of next to nothing
+    p = torch.ones(600, device=DEV)
+    opt = AdamW([p], lr=LR, state_bits=8, weight_decay=0.0)
+    g = torch.zeros(600, device=DEV)
+    g[256:] = 1e-25
+    opt.step([g])
+    assert bool((p[:256] == 1).all()) and bool(torch.isfinite(p).all())
+    assert opt.v_scale[0].tolist()[0] == 0 and bool(torch.isfinite(opt.v[0].float()).all())
+
+
+def test_adamw_refuses_shared_and_wrong_tensors():
+    buf = torch.zeros(1024, device=DEV)
+    with pytest.raises(ValueError, match="share memory"):
+        AdamW([buf[:512], buf[256:]])
+    with pytest.raises(ValueError, match="share memory"):
+        AdamW([buf, buf])
+    with pytest.raises(ValueError, match="contiguous"):
+        AdamW([torch.zeros(8, 8, device=DEV).t()])
+    with pytest.raises(TypeError):
+        AdamW([torch.zeros(8, device=DEV, dtype=torch.float16)])
+    opt = AdamW([buf])
+    for bad in ([], [torch.zeros(1023, device=DEV)] , [buf, buf]):
+        with pytest.raises(ValueError):
+            opt.step(bad)
+    for bad in (torch.zeros(1024), torch.zeros(1024, device=DEV, dtype=torch.float16), None):
+        with pytest.raises(TypeError):
+            opt.step([bad])
+    with pytest.raises(N.MoeError):                     # an address off its 16 bytes
+        AdamW([buf[1:1000]]).step([torch.zeros(999, device=DEV)])
+
+
+# -------------------------------------------------------------------- streams and graphs
+def test_captured_step_replays_with_new_data():
+    """Every operator captured in one graph on a side stream, replayed on new inputs, against
+    eager calls on the same inputs."""
+    T, d, E, k = 200, 512, 16, 4
+    wl = workload(T, d=d, E=E, k=k)
+    a = on_gpu(norm_inputs(T, d, torch.bfloat16, torch.float32, "all"))
+    logits, ids, gates = (t.to(DEV) for t in router_inputs(T, E, k))
+    R_max = N.moe_workspace_size(wl, N.MOE_WS_ROWS)
+    o = torch.randn(R_max, d, generator=gen(1)).bfloat16().to(DEV)
+    tok_row = rows_of(ids.cpu(), E, wl.beta).to(DEV)
+    dh, dx = torch.randn(T, d, generator=gen(2)).bfloat16().to(DEV), torch.randn(T, d, device=DEV)
+    dloss = torch.ones(2, device=DEV)
+
+    def build():
+        r, n = RouterLoss(wl, device=DEV), BlockNorm(wl, train=True, device=DEV)
+        w = [torch.ones(5000, device=DEV), torch.ones(300, device=DEV, dtype=torch.bfloat16)]
+        opt = AdamW(w, lr=LR, state_bits=8)
+
+        def step():
+            n(**a)
+            r(logits, ids)
+            g = n.backward(n.h_out, y=a["y"], gate=a["gate"], w_post=a["w_post"],
+                           w_next=a["w_next"], dh_out=dh, dx=dx)
+            r.backward(logits, ids, gates, dloss=dloss, dy=g.dy, o=o, tok_row=tok_row)
+            opt.step([g.dy.view(-1)[:5000], g.dy.view(-1)[5000 + 24:5324]])
+            return [n.h_out, n.x, r.losses, r.counts, *g, r.dlogits, r.dgates, *w, *opt.m,
+                    *opt.v_scale, opt.steps]
+        return step, opt
+
+    eager, e_opt = build()
+    step, g_opt = build()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    eager()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for turn in range(3):
+        a["y"].normal_()
+        logits.normal_()
+        for opt in (e_opt, g_opt):
+            opt.set_lr(LR / (turn + 1))
+        graph.replay()
+        want = eager()
+        torch.cuda.synchronize()
+        assert g_opt.steps.tolist()[:2] == [turn + 2, 0]
+        for x, y in zip(got, want):
+            assert torch.equal(x.view(torch.uint8) if x.element_size() == 1 else x,
+                               y.view(torch.uint8) if y.element_size() == 1 else y)
+
+
+def test_two_streams_at_once():
+    """Objects of their own on two streams, many calls in flight: the results of one stream."""
+    wl = workload(3000, d=1024, E=64, k=8)
+    logits, ids, _ = (t.to(DEV) for t in router_inputs(3000, 64, 8))
+    a = on_gpu(norm_inputs(3000, 1024, torch.bfloat16, torch.bfloat16, "all"))
+    dx = torch.randn(3000, 1024, generator=gen(1)).to(DEV)
+
+    def work(obj):
+        r, n = obj
+        r(logits, ids)
+        n(**a)
+        n.backward(n.h_out, y=a["y"], gate=a["gate"], w_post=a["w_post"], w_next=a["w_next"],
+                   dx=dx)
+
+    objs = [(RouterLoss(wl, device=DEV),
+             BlockNorm(wl, w_dtype=torch.bfloat16, train=True, device=DEV)) for _ in range(3)]
+    work(objs[0])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for s, obj in zip(streams, objs[1:]):
+            with torch.cuda.stream(s):
+                work(obj)
+    torch.cuda.synchronize()
+    for r, n in objs[1:]:
+        for x, y in ((r.losses, objs[0][0].losses), (r.probs, objs[0][0].probs),
+                     (n.x, objs[0][1].x), (n.dy, objs[0][1].dy),
+                     (n.dw_post, objs[0][1].dw_post), (n.dw_next, objs[0][1].dw_next)):
+            assert torch.equal(x, y)
+    # a stream that is passed, and one of no device of these arrays
+    with torch.cuda.stream(streams[0]):
+        objs[1][0](logits, ids, stream=streams[1])
+    torch.cuda.synchronize()
+    assert torch.equal(objs[1][0].losses, objs[0][0].losses)
+
+
+# ----------------------------------------------------------------------- refused arguments
+def test_wrong_arguments_are_refused():
+    T, d, E, k = 64, 256, 8, 2
+    wl = workload(T, d=d, E=E, k=k)
+    logits, ids, gates = (t.to(DEV) for t in router_inputs(T, E, k))
+    r = RouterLoss(wl, n_seq=2, device=DEV)
+    off = torch.tensor([0, 30, T], dtype=torch.int32, device=DEV)
+    r(logits, ids, None, off)
+    for bad in (dict(logits=logits.half()), dict(logits=logits.cpu()), dict(logits=None),
+                dict(topk_ids=ids.long()), dict(seq_off=None), dict(seq_off=off.long()),
+                dict(token_mask=torch.ones(T, device=DEV))):
+        with pytest.raises(TypeError):
+            r(**{**dict(logits=logits, topk_ids=ids, seq_off=off), **bad})
+    for bad in (dict(logits=logits[:-1]), dict(logits=logits.t().contiguous().t()),
+                dict(seq_off=off[:2]), dict(topk_ids=ids[:, :1]),
+                dict(logits=torch.zeros(T, 2 * E, device=DEV))):
+        with pytest.raises(ValueError):
+            r(**{**dict(logits=logits, topk_ids=ids, seq_off=off), **bad})
+    with pytest.raises(ValueError):
+        r.backward(logits, ids, gates)
+    with pytest.raises(TypeError):
+        r.backward(logits, ids, gates, dy=torch.zeros(T, d, device=DEV))
+    a = on_gpu(norm_inputs(T, d, torch.bfloat16, torch.float32, "all"))
+    n = BlockNorm(wl, device=DEV)
+    for bad in (dict(h=a["h"].float()), dict(y=a["y"].bfloat16()), dict(w_post=a["w_post"].half()),
+                dict(gate=a["gate"].cpu())):
+        with pytest.raises(TypeError):
+            n(**{**a, **bad})
+    for bad in (dict(y=None), dict(w_next=a["w_next"][:-8]), dict(h=a["h"][:, ::2]),
+                dict(gate=a["gate"][:-1])):
+        with pytest.raises(ValueError):
+            n(**{**a, **bad})
+    with pytest.raises(ValueError):
+        n(a["h"])
+    with pytest.raises(ValueError):
+        n.backward(a["h"], dh_out=a["h"])                # built without train
+    t = BlockNorm(wl, train=True, device=DEV)
+    for bad in (dict(), dict(dh_out=a["h"], dx=a["y"]), dict(w_next=a["w_next"]),
+                dict(dh_out=a["h"], gate=a["gate"])):
+        with pytest.raises(ValueError):
+            t.backward(a["h"], **bad)
+
+
+def test_rows_around_the_outputs_stay():
+    """Guard elements around every output of the C ABI calls stay as they were."""
+    T, d, E, k, G = 37, 264, 12, 3, 64
+    wl = workload(T, d=d, E=E, k=k)
+    cfg = N.MoeCfg.of(wl)
+    a = on_gpu(norm_inputs(T, d, torch.bfloat16, torch.float32, "all"))
+    logits, ids, gates = (t.to(DEV) for t in router_inputs(T, E, k))
+    guards = []
+
+    def out(n, dt=torch.float32):
+        buf = torch.full((G + n + G,), 77, dtype=dt, device=DEV)
+        guards.append((buf, n))
+        return buf[G:G + n]
+
+    status = torch.zeros(4, dtype=torch.int32, device=DEV)
+    ws = out(N.moet_workspace_size(wl, 1, N.MOET_WS_BALANCE), torch.uint8)
+    losses, counts, probs = out(4), out(E, torch.int32), out(E)
+    info, lse, dlogits, dgates = out(3, torch.int32), out(T), out(T * E), out(T * k)
+    N.moet_balance_loss(cfg, logits, ids, None, None, 1, losses, counts, probs, info, lse, ws,
+                        status)
+    R_max = N.moe_workspace_size(wl, N.MOE_WS_ROWS)
+    o = torch.zeros(R_max, d, dtype=torch.bfloat16, device=DEV)
+    N.moet_router_backward(cfg, logits, ids, gates, a["y"], o, rows_of(ids.cpu(), E, 64).to(DEV),
+                           None, None, 1, counts, info, lse, losses, dgates, dlogits, status)
+    norm = N.MoetNorm(1e-6, 0, 1, 1, N.MOET_BF16, N.MOET_F32)
+    h_out, x = out(T * d, torch.bfloat16), out(T * d, torch.bfloat16)
+    N.moet_block_norm(cfg, norm, a["h"], a["y"], a["gate"], a["w_post"], a["w_next"], h_out, x)
+    dh, dy, dgate, dwp, dwn = out(T * d, torch.bfloat16), out(T * d), out(T), out(d), out(d)
+    ws2 = out(N.moet_workspace_size(wl, 1, N.MOET_WS_NORM_BWD), torch.uint8)
+    N.moet_block_norm_backward(cfg, norm, h_out, a["y"], a["gate"], a["w_post"], a["w_next"],
+                               a["h"], a["y"], dh, dy, dgate, dwp, dwn, ws2)
+    for n in (1, 255, 257, 4099):
+        for bits, dt in ((32, torch.float32), (8, torch.uint8)):
+            nb = -(-n // 256)
+            p, m, v = out(n, torch.bfloat16), out(n, dt), out(n, dt)
+            sm, sv = (out(nb), out(nb)) if bits == 8 else (None, None)
+            mw = out(n)
+            for t in (m, v, sm, sv):
+                if t is not None:
+                    t.zero_()
+            g = torch.ones(n, device=DEV)
+            ptr = lambda t: None if t is None else t.data_ptr()
+            e = (N.MoetAdamwTensor * 1)(N.MoetAdamwTensor(
+                ptr(p), ptr(g), ptr(m), ptr(v), ptr(sm), ptr(sv), ptr(mw), n, 0.1, N.MOET_BF16,
+                N.MOET_F32, N.MOET_F32 if bits == 32 else N.MOET_E4M3))
+            steps = torch.zeros(4, dtype=torch.int32, device=DEV)
+            N.moet_adamw_step(e, 1, N.MoetAdamw(0.9, 0.95, 1e-8),
+                              torch.full((4,), 1e-3, device=DEV), None, steps)
+            torch.cuda.synchronize()
+            assert bool((mw < 77).all())
+    torch.cuda.synchronize()
+    for buf, n in guards:
+        assert bool((buf[:G] == 77).all()) and bool((buf[G + n:] == 77).all())
