@@ -141,7 +141,8 @@ MOE_API int moet_block_norm_backward(const moe_cfg* cfg, const moet_norm* norm,
  *   m, v   the moments, updated.  state_dtype MOET_F32: fp32 [n] each, v the second moment.
  *          MOET_E4M3: one byte an element; block b of MOET_ADAMW_BLOCK elements stands for
  *          m[i] * m_scale[b], and v for the second moment's root, v[i] * v_scale[b].
- *   m_scale, v_scale fp32 [ceil(n / MOET_ADAMW_BLOCK)], updated (NULL with MOET_F32). */
+ *   m_scale, v_scale fp32 [ceil(n / MOET_ADAMW_BLOCK)], updated, 4-byte aligned (NULL with
+ *          MOET_F32). */
 typedef struct moet_adamw_tensor {
   void* p;
   const void* g;

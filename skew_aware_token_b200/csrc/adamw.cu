@@ -21,6 +21,7 @@
 #include <cuda_fp8.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "train_common.cuh"
 
@@ -59,100 +60,252 @@ constexpr int kCaps[3] = {8, 64, 400};
 static_assert(sizeof(Batch<400>) <= 32000, "launch parameters");
 
 struct Consts {
-  float b1, b2, omb1, omb2, log_b1, log_b2, eps;
+  float b1, b2, omb1, omb2, log_b1, log_b2, eps, one;
 };
 
-__device__ __forceinline__ void load4(const float* p, long long i, long long n, float* v) {
-  if (i + 4 <= n) {
-    const float4 a = *reinterpret_cast<const float4*>(p + i);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = i + j < n ? p[i + j] : 0.f;
-  }
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, long long i, long long n,
-                                      float* v) {
-  if (i + 4 <= n) {
-    const uint2 a = *reinterpret_cast<const uint2*>(p + i);
-    v[0] = __uint_as_float(a.x << 16), v[1] = __uint_as_float(a.x & 0xffff0000u);
-    v[2] = __uint_as_float(a.y << 16), v[3] = __uint_as_float(a.y & 0xffff0000u);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = i + j < n ? __bfloat162float(p[i + j]) : 0.f;
-  }
-}
-__device__ __forceinline__ uint32_t load4_codes(const uint8_t* p, long long i, long long n) {
-  if (i + 4 <= n) return *reinterpret_cast<const uint32_t*>(p + i);
-  uint32_t w = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (i + j < n) w |= (uint32_t)p[i + j] << (8 * j);
-  return w;
-}
-__device__ __forceinline__ void decode4(uint32_t w, float* v) {
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-        (__nv_fp8x2_storage_t)(w >> (16 * j)), __NV_E4M3);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    v[2 * j] = f.x, v[2 * j + 1] = f.y;
-  }
-}
-__device__ __forceinline__ uint32_t encode4(const float* v) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE,
-                                               __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE,
-                                               __NV_E4M3);
-  return lo | hi << 16;
-}
-__device__ __forceinline__ void store4(float* p, long long i, long long n, const float* v) {
-  if (i + 4 <= n) {
-    *reinterpret_cast<float4*>(p + i) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (i + j < n) p[i + j] = v[j];
-  }
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, long long i, long long n,
-                                       const float* v) {
-  if (i + 4 <= n) {
-    *reinterpret_cast<uint2*>(p + i) =
-        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (i + j < n) p[i + j] = __float2bfloat16_rn(v[j]);
-  }
-}
-__device__ __forceinline__ void store4_codes(uint8_t* p, long long i, long long n,
-                                             uint32_t w) {
-  if (i + 4 <= n) {
-    *reinterpret_cast<uint32_t*>(p + i) = w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (i + j < n) p[i + j] = (uint8_t)(w >> (8 * j));
-  }
-}
+// A lane's 8 elements of a block, as 4 pairs.  With 8-bit states they are consecutive (one
+// load of 8 codes, one or two of the rest); with fp32 states two runs of 4, one in either
+// half of the block, so that the loads of 16 bytes stay consecutive over the lanes.
+// FULL: the whole block lies inside the tensor.
+template <bool S8>
+struct Lane {
+  long long at, n;  // the first element, the tensor's length
+  __device__ Lane(long long block, int lane, long long n)
+      : at(block * kBlock + lane * (S8 ? 8 : 4)), n(n) {}
+  __device__ long long index(int i) const { return at + (S8 || i < 4 ? i : kBlock / 2 + i - 4); }
 
+  template <bool FULL>
+  __device__ void load(const float* p, float2 (&v)[4]) const {
+    if constexpr (FULL) {
+      const float4 a = *reinterpret_cast<const float4*>(p + at);
+      const float4 b = *reinterpret_cast<const float4*>(p + index(4));
+      v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w);
+      v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = make_float2(index(2 * i) < n ? p[index(2 * i)] : 0.f,
+                           index(2 * i + 1) < n ? p[index(2 * i + 1)] : 0.f);
+    }
+  }
+  template <bool FULL>
+  __device__ void load(const __nv_bfloat16* p, float2 (&v)[4]) const {
+    if constexpr (FULL) {
+      uint4 a;
+      if constexpr (S8) {
+        a = *reinterpret_cast<const uint4*>(p + at);
+      } else {
+        const uint2 lo = *reinterpret_cast<const uint2*>(p + at);
+        const uint2 hi = *reinterpret_cast<const uint2*>(p + index(4));
+        a = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      }
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = make_float2(
+            index(2 * i) < n ? __bfloat162float(p[index(2 * i)]) : 0.f,
+            index(2 * i + 1) < n ? __bfloat162float(p[index(2 * i + 1)]) : 0.f);
+    }
+  }
+  template <bool FULL>
+  __device__ void load(const uint8_t* p, float2 (&v)[4]) const {
+    uint32_t w[2] = {0, 0};
+    if constexpr (FULL) {
+      const uint2 a = *reinterpret_cast<const uint2*>(p + at);
+      w[0] = a.x, w[1] = a.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (index(i) < n) w[i / 4] |= (uint32_t)p[index(i)] << (8 * (i % 4));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+          (__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i % 2))), __NV_E4M3);
+      v[i] = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    }
+  }
+  template <bool FULL>
+  __device__ void store(float* p, const float2 (&v)[4]) const {
+    if constexpr (FULL) {
+      *reinterpret_cast<float4*>(p + at) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+      *reinterpret_cast<float4*>(p + index(4)) = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (index(2 * i) < n) p[index(2 * i)] = v[i].x;
+        if (index(2 * i + 1) < n) p[index(2 * i + 1)] = v[i].y;
+      }
+    }
+  }
+  template <bool FULL>
+  __device__ void store(__nv_bfloat16* p, const float2 (&v)[4]) const {
+    if constexpr (FULL) {
+      const uint2 lo = make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y));
+      const uint2 hi = make_uint2(pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+      if constexpr (S8) {
+        *reinterpret_cast<uint4*>(p + at) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      } else {
+        *reinterpret_cast<uint2*>(p + at) = lo;
+        *reinterpret_cast<uint2*>(p + index(4)) = hi;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (index(2 * i) < n) p[index(2 * i)] = __float2bfloat16_rn(v[i].x);
+        if (index(2 * i + 1) < n) p[index(2 * i + 1)] = __float2bfloat16_rn(v[i].y);
+      }
+    }
+  }
+  template <bool FULL>
+  __device__ void store(uint8_t* p, const float2 (&v)[4]) const {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      w[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(v[2 * i], __NV_SATFINITE, __NV_E4M3) |
+             (uint32_t)__nv_cvt_float2_to_fp8x2(v[2 * i + 1], __NV_SATFINITE, __NV_E4M3) << 16;
+    if constexpr (FULL) {
+      *reinterpret_cast<uint2*>(p + at) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (index(i) < n) p[index(i)] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+    }
+  }
+};
+
+// max(|a|, |b|, |c|), NaN if any is
+__device__ __forceinline__ float top3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // The largest of the lanes' non-negative values (NaN above infinity above all numbers).
 __device__ __forceinline__ float warp_top(float v) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two fp32 operations an instruction.
+__device__ __forceinline__ unsigned long long bits2(float2 a) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 pair(unsigned long long r) {
+  float2 a;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
+  return a;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return pair(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return pair(r);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+struct Step {
+  float gs, lr, lr1, inv2;  // gradient scale, lr, lr / (1 - b1^t), (1 - b2^t)^-1/2
+  bool scaled;
+};
+
+// One block of one tensor by one warp.
+template <int W, bool GBF16, bool S8, bool FULL>
+__device__ __forceinline__ void update_block(const Item& it, long long block, int lane,
+                                             const Consts& c, const Step& st) {
+  using G = typename std::conditional<GBF16, __nv_bfloat16, float>::type;
+  using P = typename std::conditional<W == W_F32, float, __nv_bfloat16>::type;
+  using M = typename std::conditional<S8, uint8_t, float>::type;
+  const Lane<S8> at(block, lane, it.n);
+  float2 g[4], p[4], m[4], v[4];
+  at.template load<FULL>(static_cast<const G*>(it.g), g);
+  if constexpr (W == W_BF16_MASTER) at.template load<FULL>(it.master, p);
+  else at.template load<FULL>(static_cast<const P*>(it.p), p);
+  at.template load<FULL>(static_cast<const M*>(it.m), m);
+  at.template load<FULL>(static_cast<const M*>(it.v), v);
+  float sm = 0.f, sv = 0.f;
+  if constexpr (S8) {
+    sm = it.m_scale[block];
+    sv = it.v_scale[block];
+  }
+  const float2 decay = both(fmaf(-st.lr, it.wd, 1.f)), by = both(-st.lr1);
+  float2 r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (S8) {
+      m[i] = mul2(m[i], both(sm));
+      v[i] = mul2(v[i], both(sv));
+      v[i] = mul2(v[i], v[i]);
+    }
+    if (st.scaled) g[i] = mul2(g[i], both(st.gs));
+    // Sums of two rounded products: as a * one + b with a `one` that the compiler cannot see,
+    // since it fuses a packed product and sum (even with .rn) into one rounding.
+    m[i] = fma2(mul2(m[i], both(c.b1)), both(c.one), mul2(g[i], both(c.omb1)));
+    v[i] = fma2(mul2(v[i], both(c.b2)), both(c.one), mul2(mul2(g[i], both(c.omb2)), g[i]));
+    r[i] = make_float2(__fsqrt_rn(v[i].x), __fsqrt_rn(v[i].y));
+    const float2 den = fma2(r[i], both(st.inv2), both(c.eps));
+    const float2 q = mul2(m[i], make_float2(reciprocal(den.x), reciprocal(den.y)));
+    p[i] = fma2(by, q, mul2(p[i], decay));
+  }
+  at.template store<FULL>(static_cast<P*>(it.p), p);
+  if constexpr (W == W_BF16_MASTER) at.template store<FULL>(it.master, p);
+  if constexpr (S8) {
+    float top_m = 0.f, top_r = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      top_m = top3(m[i].x, m[i].y, top_m);
+      top_r = top3(r[i].x, r[i].y, top_r);
+    }
+    top_m = warp_top(top_m);
+    top_r = warp_top(top_r);
+    const bool some_m = !(top_m < kLeastTop), some_r = !(top_r < kLeastTop);
+    const float im = some_m ? __fmul_rn(kE4m3Max, __frcp_rn(top_m)) : 0.f;
+    const float ir = some_r ? __fmul_rn(kE4m3Max, __frcp_rn(top_r)) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = mul2(m[i], both(im));
+      // a positive root is 2^-75 and more: min(r * 1e38, tiny) is tiny for it, 0 for 0
+      const float2 least = mul2(r[i], both(1e38f));
+      v[i] = mul2(r[i], both(ir));
+      v[i].x = fmaxf(v[i].x, fminf(least.x, kE4m3Tiny));
+      v[i].y = fmaxf(v[i].y, fminf(least.y, kE4m3Tiny));
+    }
+    if (lane == 0) {
+      it.m_scale[block] = some_m ? __fmul_rn(top_m, 1.f / kE4m3Max) : 0.f;
+      it.v_scale[block] = some_r ? __fmul_rn(top_r, 1.f / kE4m3Max) : 0.f;
+    }
+  }
+  at.template store<FULL>(static_cast<M*>(it.m), m);
+  at.template store<FULL>(static_cast<M*>(it.v), v);
+}
 
 template <int W, bool GBF16, bool S8, int CAP>
-__global__ void __launch_bounds__(kThreads)
-adamw_kernel(const __grid_constant__ Batch<CAP> b, const Consts c, const float* lr_p,
-             const float* grad_scale, int32_t* step, bool last_launch) {
+__global__ void __launch_bounds__(kThreads, 4)
+adamw_kernel(const __grid_constant__ Batch<CAP> b, const __grid_constant__ Consts c,
+             const float* lr_p, const float* grad_scale, int32_t* step, bool last_launch) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float gs = grad_scale ? *grad_scale : 1.f;
-  if (!isfinite(gs)) return;  // the same for every CTA: the step is left out as a whole
+  Step st;
+  st.scaled = grad_scale != nullptr;
+  st.gs = st.scaled ? *grad_scale : 1.f;
+  if (!isfinite(st.gs)) return;  // the same for every CTA: the step is left out as a whole
   const int t = step[0] + 1;
-  const float lr = *lr_p;
-  const float lr1 = lr / -expm1f((float)t * c.log_b1);
-  const float inv2 = rsqrtf(-expm1f((float)t * c.log_b2));
+  st.lr = *lr_p;
+  st.lr1 = st.lr / -expm1f((float)t * c.log_b1);
+  st.inv2 = rsqrtf(-expm1f((float)t * c.log_b2));
   const int tiles = b.first_tile[b.count];
 
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -163,91 +316,9 @@ adamw_kernel(const __grid_constant__ Batch<CAP> b, const Consts c, const float* 
       else hi = mid - 1;
     }
     const Item& it = b.item[lo];
-    const long long n = it.n;
     const long long block = (long long)(tile - b.first_tile[lo]) * (kThreads / 32) + warp;
-    if (block * kBlock >= n) continue;
-    const float decay = fmaf(-lr, it.wd, 1.f);
-    long long at[2];
-    float g[2][4], p[2][4], m[2][4], v[2][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      at[h] = block * kBlock + h * (kBlock / 2) + lane * 4;
-      if (GBF16) load4(static_cast<const __nv_bfloat16*>(it.g), at[h], n, g[h]);
-      else load4(static_cast<const float*>(it.g), at[h], n, g[h]);
-      if (W == W_F32) load4(static_cast<const float*>(it.p), at[h], n, p[h]);
-      else if (W == W_BF16) load4(static_cast<const __nv_bfloat16*>(it.p), at[h], n, p[h]);
-      else load4(it.master, at[h], n, p[h]);
-      if (S8) {
-        decode4(load4_codes(static_cast<const uint8_t*>(it.m), at[h], n), m[h]);
-        decode4(load4_codes(static_cast<const uint8_t*>(it.v), at[h], n), v[h]);
-      } else {
-        load4(static_cast<const float*>(it.m), at[h], n, m[h]);
-        load4(static_cast<const float*>(it.v), at[h], n, v[h]);
-      }
-    }
-    float sm = 0.f, sv = 0.f, top_m = 0.f, top_r = 0.f;
-    if (S8) {
-      sm = it.m_scale[block];
-      sv = it.v_scale[block];
-    }
-    float r[2][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float mo = m[h][j], vo = v[h][j];
-        if (S8) {
-          mo = __fmul_rn(mo, sm);
-          vo = __fmul_rn(vo, sv);
-          vo = __fmul_rn(vo, vo);
-        }
-        const float gr = grad_scale ? __fmul_rn(g[h][j], gs) : g[h][j];
-        mo = __fadd_rn(__fmul_rn(mo, c.b1), __fmul_rn(gr, c.omb1));
-        vo = __fadd_rn(__fmul_rn(vo, c.b2), __fmul_rn(__fmul_rn(gr, c.omb2), gr));
-        const float root = __fsqrt_rn(vo);
-        const float step_by = __fdividef(mo, fmaf(root, inv2, c.eps));
-        p[h][j] = fmaf(-lr1, step_by, p[h][j] * decay);
-        m[h][j] = mo;
-        v[h][j] = vo;
-        r[h][j] = root;
-        if (S8) {
-          // as bit patterns: a NaN stays the largest
-          top_m = __uint_as_float(max(__float_as_uint(top_m), __float_as_uint(fabsf(mo))));
-          top_r = __uint_as_float(max(__float_as_uint(top_r), __float_as_uint(root)));
-        }
-      }
-    if (S8) {
-      top_m = warp_top(top_m);
-      top_r = warp_top(top_r);
-      const bool some_m = !(top_m < kLeastTop), some_r = !(top_r < kLeastTop);
-      const float im = some_m ? __fmul_rn(kE4m3Max, __frcp_rn(top_m)) : 0.f;
-      const float ir = some_r ? __fmul_rn(kE4m3Max, __frcp_rn(top_r)) : 0.f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          m[h][j] = __fmul_rn(m[h][j], im);
-          const float code = __fmul_rn(r[h][j], ir);
-          v[h][j] = r[h][j] > 0.f ? fmaxf(code, kE4m3Tiny) : code;
-        }
-      if (lane == 0) {
-        it.m_scale[block] = some_m ? __fmul_rn(top_m, 1.f / kE4m3Max) : 0.f;
-        it.v_scale[block] = some_r ? __fmul_rn(top_r, 1.f / kE4m3Max) : 0.f;
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (W == W_F32) store4(static_cast<float*>(it.p), at[h], n, p[h]);
-      else store4(static_cast<__nv_bfloat16*>(it.p), at[h], n, p[h]);
-      if (W == W_BF16_MASTER) store4(it.master, at[h], n, p[h]);
-      if (S8) {
-        store4_codes(static_cast<uint8_t*>(it.m), at[h], n, encode4(m[h]));
-        store4_codes(static_cast<uint8_t*>(it.v), at[h], n, encode4(v[h]));
-      } else {
-        store4(static_cast<float*>(it.m), at[h], n, m[h]);
-        store4(static_cast<float*>(it.v), at[h], n, v[h]);
-      }
-    }
+    if ((block + 1) * kBlock <= it.n) update_block<W, GBF16, S8, true>(it, block, lane, c, st);
+    else if (block * kBlock < it.n) update_block<W, GBF16, S8, false>(it, block, lane, c, st);
   }
   // The last CTA to end raises the step count: all have read it by then.  The ticket wraps
   // to 0 by itself, so nothing has to be cleared between calls.
@@ -322,7 +393,7 @@ cudaError_t launch_adamw(const moet_adamw_tensor* tensors, int count, const moet
   const Consts c = {(float)opt.beta1,           (float)opt.beta2,
                     (float)(1.0 - opt.beta1),   (float)(1.0 - opt.beta2),
                     (float)std::log(opt.beta1), (float)std::log(opt.beta2),
-                    (float)opt.eps};
+                    (float)opt.eps,             1.f};
   // the launches: runs of tensors of one kind, cut at the largest capacity and at 2^30 tiles
   // (a launch that raises the count goes last, with no tensors if there are none)
   const moet_adamw_tensor* run[kCaps[2]];

@@ -62,11 +62,11 @@ __global__ void __launch_bounds__(1024)
 block_norm_kernel(const NormArgs a, const HT* h, const float* __restrict__ y,
                   const float* __restrict__ gate, const WT* __restrict__ w_post,
                   const WT* __restrict__ w_next, HT* h_out, __nv_bfloat16* __restrict__ x) {
-  extern __shared__ float smem[];
+  extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x & 31;
   const int group = (threadIdx.x >> 5) / a.W, warp = (threadIdx.x >> 5) % a.W;
   const int groups = (blockDim.x >> 5) / a.W;
-  float* red = smem + group * 64;
+  float* red = reinterpret_cast<float*>(smem) + group * 64;
   float wp[V][8], wn[V][8];
   bool in[V];
 #pragma unroll
@@ -129,95 +129,201 @@ block_norm_kernel(const NormArgs a, const HT* h, const float* __restrict__ y,
   }
 }
 
-// A thread owns 8 columns of every row of its group.
+// 8 elements of one row in a thread's slots: one 16-byte unit of bf16 or two of fp32, units a
+// CTA's width apart (consecutive lanes read consecutive 16 bytes).
+template <class T>
+struct Slots {
+  static constexpr int kUnits = sizeof(T) * 8 / 16;
+  __device__ static void fill(uint32_t slot, uint32_t pitch, const T* src) {
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+      copy_ahead16(slot + i * pitch, reinterpret_cast<const char*>(src) + 16 * i);
+  }
+  __device__ static void read(uint32_t slot, uint32_t pitch, float* v) {
+    if constexpr (kUnits == 1) {
+      bf16x8_to_f32(slot16(slot), v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 a = slot16(slot + i * pitch);
+        v[4 * i] = __uint_as_float(a.x), v[4 * i + 1] = __uint_as_float(a.y);
+        v[4 * i + 2] = __uint_as_float(a.z), v[4 * i + 3] = __uint_as_float(a.w);
+      }
+    }
+  }
+};
+
+// The six sums of a row over its group of W warps, on every thread.  `red`: 8 * 17 floats.
+__device__ __forceinline__ void group_sum8(float (&v)[8], int W, int group, int warp, int lane,
+                                           float* red) {
+  float s = warp_sum8(v, lane);
+  if (W > 1) {
+    if ((lane & 3) == 0) red[(lane >> 2) * 17 + warp] = s;
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(W * 32) : "memory");
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int w = (lane & 3) + 4 * i;
+      if (w < W) s += red[(lane >> 2) * 17 + w];
+    }
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+  }
+#pragma unroll
+  for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(0xffffffffu, s, 4 * i);
+}
+
+constexpr int kBwdV = 2;                        // 8-column steps of a thread
+constexpr int kBwdThreads = 512;
+constexpr int kBwdRed = 2 * 8 * 17;             // floats of a group's two reduction buffers
+template <class HT>
+constexpr int bwd_units() {                     // 16-byte units of a thread: a row and weights
+  return kBwdV * (2 * Slots<HT>::kUnits + 4 + 4);
+}
+
+// A thread owns 16 columns of every row of its group.  The next row's columns are copied to
+// the thread's slots while this row is worked on (no thread reads another's slots).
 template <class HT, class WT>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(kBwdThreads)
 block_norm_backward_kernel(const NormArgs a, const HT* __restrict__ h_out,
                            const float* __restrict__ y, const float* __restrict__ gate,
                            const WT* __restrict__ w_post, const WT* __restrict__ w_next,
                            const HT* dh_out, const float* __restrict__ dx, HT* dh,
                            float* __restrict__ dy, float* __restrict__ dgate,
                            float* __restrict__ partial) {
-  extern __shared__ float smem[];
+  constexpr int V = kBwdV, HU = Slots<HT>::kUnits;
+  extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x & 31;
   const int group = (threadIdx.x >> 5) / a.W, warp = (threadIdx.x >> 5) % a.W;
   const int groups = (blockDim.x >> 5) / a.W;
-  float* red = smem + group * (2 * 6 * 32);
-  const int v = warp * 32 + lane;
-  const bool in = v < a.d8;
-  float wp[8], wn[8], gp[8], gn[8];
-  load_weight(w_post, v, in, a.w_offset, wp);
-  load_weight(w_next, v, in, a.w_offset, wn);
+  const uint32_t pitch = blockDim.x * 16;
+  const uint32_t slots = smem_addr(smem) + threadIdx.x * 16;
+  float* red = reinterpret_cast<float*>(smem + bwd_units<HT>() * pitch) + group * kBwdRed;
+  // unit offsets: h', dh', y, dx, then the weights
+  auto slot = [&](int unit) { return slots + (uint32_t)unit * pitch; };
+  constexpr int kH = 0, kDh = V * HU, kY = 2 * V * HU, kDx = kY + 2 * V, kWp = kDx + 2 * V,
+                kWn = kWp + 2 * V;
+  bool in[V];
+  float gp[V][8], gn[V][8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) gp[j] = gn[j] = 0.f;
-  int turn = 0;
-  for (int t = blockIdx.x * groups + group; t < a.T; t += gridDim.x * groups, turn ^= 1) {
-    const long long at = ((long long)t * a.d8 + v) * 8;
-    float hv[8], yv[8], q[8], u[8];
+  for (int u = 0; u < V; ++u) {
+    const int v = (u * a.W + warp) * 32 + lane;
+    in[u] = v < a.d8;
+    float w[8];
+    float4* q = reinterpret_cast<float4*>(smem) + threadIdx.x;
+    load_weight(w_post, v, in[u], a.w_offset, w);
+    q[(kWp + 2 * u) * blockDim.x] = make_float4(w[0], w[1], w[2], w[3]);
+    q[(kWp + 2 * u + 1) * blockDim.x] = make_float4(w[4], w[5], w[6], w[7]);
+    load_weight(w_next, v, in[u], a.w_offset, w);
+    q[(kWn + 2 * u) * blockDim.x] = make_float4(w[0], w[1], w[2], w[3]);
+    q[(kWn + 2 * u + 1) * blockDim.x] = make_float4(w[4], w[5], w[6], w[7]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) hv[j] = yv[j] = q[j] = u[j] = 0.f;
-    if (in) {
-      if (w_next) load8(h_out + at, hv);
-      if (y) load8(y + at, yv);
-      if (dh_out) load8(dh_out + at, u);
-      if (w_next) load8(dx + at, q);
+    for (int i = 0; i < kWp; ++i) q[i * blockDim.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) gp[u][j] = gn[u][j] = 0.f;
+  }
+  auto ahead = [&](int t) {
+    if (t < a.T) {
+#pragma unroll
+      for (int u = 0; u < V; ++u) {
+        if (!in[u]) continue;
+        const long long at = ((long long)t * a.d8 + (u * a.W + warp) * 32 + lane) * 8;
+        if (w_next) Slots<HT>::fill(slot(kH + u * HU), pitch, h_out + at);
+        if (dh_out) Slots<HT>::fill(slot(kDh + u * HU), pitch, dh_out + at);
+        if (y) Slots<float>::fill(slot(kY + 2 * u), pitch, y + at);
+        if (w_next) Slots<float>::fill(slot(kDx + 2 * u), pitch, dx + at);
+      }
     }
-    float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    commit_copies();
+  };
+  const int step = gridDim.x * groups;
+  int t = blockIdx.x * groups + group, turn = 0;
+  ahead(t);
+  for (; t < a.T; t += step, turn ^= 1) {
+    float hv[V][8], yv[V][8], q[V][8], u8[V][8];
+    const float gt = gate ? gate[t] : 1.f;
+    wait_copies<0>();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float qw = q[j] * wn[j], yw = yv[j] * wp[j];
-      s[0] = fmaf(hv[j], hv[j], s[0]);
-      s[1] = fmaf(qw, hv[j], s[1]);
-      s[2] = fmaf(yv[j], yv[j], s[2]);
-      s[3] = fmaf(u[j], yw, s[3]);
-      s[4] = fmaf(qw, yw, s[4]);
-      s[5] = fmaf(hv[j], yw, s[5]);
+    for (int u = 0; u < V; ++u) {
+      Slots<HT>::read(slot(kH + u * HU), pitch, hv[u]);
+      Slots<HT>::read(slot(kDh + u * HU), pitch, u8[u]);
+      Slots<float>::read(slot(kY + 2 * u), pitch, yv[u]);
+      Slots<float>::read(slot(kDx + 2 * u), pitch, q[u]);
     }
-    group_sum(s, a.W, group, warp, lane, red + turn * (6 * 32));
+    ahead(t + step);
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      float wp[8], wn[8];
+      Slots<float>::read(slot(kWp + 2 * u), pitch, wp);
+      Slots<float>::read(slot(kWn + 2 * u), pitch, wn);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float qw = q[u][j] * wn[j], yw = yv[u][j] * wp[j];
+        s[0] = fmaf(hv[u][j], hv[u][j], s[0]);
+        s[1] = fmaf(qw, hv[u][j], s[1]);
+        s[2] = fmaf(yv[u][j], yv[u][j], s[2]);
+        s[3] = fmaf(u8[u][j], yw, s[3]);
+        s[4] = fmaf(qw, yw, s[4]);
+        s[5] = fmaf(hv[u][j], yw, s[5]);
+      }
+    }
+    group_sum8(s, a.W, group, warp, lane, red + turn * (kBwdRed / 2));
     float A = 0.f, B = 0.f;
     if (w_next) {
       A = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
       B = A * A * A * s[1] * a.inv_d;
     }
+    const float uy = fmaf(A, s[4], fmaf(-B, s[5], s[3]));
+    const float ry = w_post ? rsqrtf(fmaf(s[2], a.inv_d, a.eps)) : 1.f;
+    const float scale = a.out_scale * gt * ry;
+    const float back = w_post ? ry * ry * uy * a.inv_d : 0.f;
+    const float res = y ? a.res_scale : 1.f;
+    if (gate && warp == 0 && lane == 0) dgate[t] = a.out_scale * ry * uy;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      gn[j] = fmaf(q[j] * hv[j], A, gn[j]);
-      u[j] = fmaf(A, q[j] * wn[j], fmaf(-B, hv[j], u[j]));
-    }
-    if (y) {
-      const float uy = fmaf(A, s[4], fmaf(-B, s[5], s[3]));
-      const float ry = w_post ? rsqrtf(fmaf(s[2], a.inv_d, a.eps)) : 1.f;
-      if (gate && threadIdx.x % (a.W * 32) == 0) dgate[t] = a.out_scale * ry * uy;
-      const float scale = a.out_scale * (gate ? gate[t] : 1.f) * ry;
-      const float back = w_post ? ry * ry * uy * a.inv_d : 0.f;
+    for (int u = 0; u < V; ++u) {
+      float wp[8], wn[8];
+      Slots<float>::read(slot(kWp + 2 * u), pitch, wp);
+      Slots<float>::read(slot(kWn + 2 * u), pitch, wn);
+      const long long at = ((long long)t * a.d8 + (u * a.W + warp) * 32 + lane) * 8;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        gp[j] = fmaf(u[j] * yv[j], scale, gp[j]);
-        yv[j] = scale * fmaf(u[j], wp[j], -yv[j] * back);
-        u[j] *= a.res_scale;
+        gn[u][j] = fmaf(q[u][j] * A, hv[u][j], gn[u][j]);
+        const float g = fmaf(q[u][j] * wn[j], A, fmaf(-B, hv[u][j], u8[u][j]));
+        gp[u][j] = fmaf(g * scale, yv[u][j], gp[u][j]);
+        yv[u][j] = scale * fmaf(g, wp[j], -yv[u][j] * back);
+        u8[u][j] = g * res;
       }
-      if (in) store8(dy + at, yv);
+      if (in[u]) {
+        if (y) store8(dy + at, yv[u]);
+        store8(dh + at, u8[u]);
+      }
     }
-    if (in) store8(dh + at, u);
   }
-  // the CTA's partial row: the groups' columns added in group order
-  float* col = smem + groups * (2 * 6 * 32);
+  // the CTA's partial row: the groups' columns added in group order, in the slots' place
+  float* col = reinterpret_cast<float*>(smem);
+  if (groups > 1) __syncthreads();
   for (int g = 0; g < groups; ++g) {
-    if (groups > 1) __syncthreads();
-    if (group == g && in) {
-      if (g > 0) {
-        float t8[8];
-        load8(col + v * 8, t8);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) gp[j] += t8[j];
-        load8(col + (a.d8 + v) * 8, t8);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) gn[j] += t8[j];
-      }
+    if (group == g) {
       float* out = g == groups - 1 ? partial + (long long)blockIdx.x * 2 * a.d8 * 8 : col;
-      store8(out + v * 8, gp);
-      store8(out + (a.d8 + v) * 8, gn);
+#pragma unroll
+      for (int u = 0; u < V; ++u) {
+        const int v = (u * a.W + warp) * 32 + lane;
+        if (!in[u]) continue;
+        if (g > 0) {
+          float t8[8];
+          load8(col + v * 8, t8);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) gp[u][j] += t8[j];
+          load8(col + (a.d8 + v) * 8, t8);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) gn[u][j] += t8[j];
+        }
+        store8(out + v * 8, gp[u]);
+        store8(out + (a.d8 + v) * 8, gn[u]);
+      }
     }
+    if (groups > 1) __syncthreads();
   }
 }
 
@@ -278,19 +384,32 @@ cudaError_t backward(const moe_cfg& c, const moet_norm& n, const void* h_out, co
                      const float* gate, const void* wp, const void* wn, const void* dh_out,
                      const float* dx, void* dh, float* dy, float* dgate, float* dw_post,
                      float* dw_next, void* ws, cudaStream_t st) {
-  const NormArgs a = make_args(c, n, 1);
-  const int groups = groups_of(a.W), threads = groups * a.W * 32;
-  const size_t smem = (size_t)groups * 2 * 6 * 32 * 4 + (groups > 1 ? 2 * (size_t)c.d * 4 : 0);
+  const NormArgs a = make_args(c, n, kBwdV);
+  const int sms = num_sms();
+  // as many row groups as fit the CTA, but no more than it takes to give every SM rows
+  int groups = kBwdThreads / 32 / a.W;
+  const int rows_per_sm = (c.T + sms - 1) / sms;
+  if (groups > rows_per_sm) groups = rows_per_sm;
+  if (groups < 1) groups = 1;
+  const int threads = groups * a.W * 32;
+  const size_t smem = (size_t)bwd_units<HT>() * threads * 16 + (size_t)groups * kBwdRed * 4;
+  auto kernel = block_norm_backward_kernel<HT, WT>;
+  static OncePerDevice once;
+  cudaError_t err = once_per_device(once, [&](int&) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                bwd_units<HT>() * kBwdThreads * 16 + 16 * kBwdRed * 4);
+  });
+  if (err != cudaSuccess) return err;
   int grid = (c.T + groups - 1) / groups;
-  const int cap = num_sms() * (2048 / threads);
+  const int cap = sms * (kBwdThreads / threads);
   if (grid > cap) grid = cap;
   if (grid > kMaxPartials) grid = kMaxPartials;
   if (grid > 0) {
-    block_norm_backward_kernel<HT, WT><<<grid, threads, smem, st>>>(
+    kernel<<<grid, threads, smem, st>>>(
         a, static_cast<const HT*>(h_out), y, gate, static_cast<const WT*>(wp),
         static_cast<const WT*>(wn), static_cast<const HT*>(dh_out), dx, static_cast<HT*>(dh),
         dy, dgate, static_cast<float*>(ws));
-    const cudaError_t err = cudaGetLastError();
+    err = cudaGetLastError();
     if (err != cudaSuccess) return err;
   }
   if (!dw_post && !dw_next) return cudaSuccess;

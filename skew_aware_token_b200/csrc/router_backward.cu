@@ -9,6 +9,10 @@
 // rows (16-byte loads, all k rows of a column in flight together) and one stride of the
 // experts; the k products and sum_i a_i p_i leave in one reduction, after which the group's
 // threads write their experts.  Bound by HBM: k d 2 bytes of O rows and d 4 of dy a token.
+// The rows' indices are read a token ahead and the logits before the rows: with the index's
+// and the logits' latency in front of the rows, 16384 tokens of 8 x 7168 took 550 us; without
+// it 356 us (2.38 GB, 6.7 TB/s: the rate of a plain copy).
+#include <type_traits>
 #include "train_common.cuh"
 
 namespace moe {
@@ -29,8 +33,9 @@ __device__ __forceinline__ uint4 ld_once(const uint4* p) {
   return v;
 }
 
-// W warps a token.  K8: k rows of O are read (k <= 8), else the losses' part alone.
-template <int W>
+// W warps a token, kEpt experts a thread.  dy == NULL: the losses' part alone; dloss == NULL:
+// the gates' part alone.
+template <int W, int kEpt>
 __global__ void __launch_bounds__(kThreads)
 router_backward_kernel(const RouterArgs a, const float* __restrict__ logits,
                        const int32_t* __restrict__ ids, const float* __restrict__ gates,
@@ -41,11 +46,17 @@ router_backward_kernel(const RouterArgs a, const float* __restrict__ logits,
                        const float* __restrict__ dloss, float* __restrict__ dgates,
                        float* __restrict__ dlogits, int32_t* __restrict__ status) {
   constexpr int kGroups = kThreads / 32 / W;
-  constexpr int kEpt = kMaxE / (32 * W);  // experts a thread
   __shared__ float red[kGroups][2][kMaxK + 1][W];
   const int lane = threadIdx.x & 31;
   const int group = (threadIdx.x >> 5) / W, warp = (threadIdx.x >> 5) % W;
   const int tid = warp * 32 + lane;
+  const int step = gridDim.x * kGroups;
+  int t = blockIdx.x * kGroups + group;
+  // lane j holds the row of the token's j-th choice, read a token ahead
+  auto row_of = [&](int token) {
+    return dy && lane < a.k && token < a.T ? __ldg(tok_row + (long long)token * a.k + lane) : 0;
+  };
+  int next_row = row_of(t);
   float b = 0.f, z = 0.f;
   if (dloss) {
     const int n = seq_info[a.n_seq], some = seq_info[a.n_seq + 1];
@@ -54,52 +65,38 @@ router_backward_kernel(const RouterArgs a, const float* __restrict__ logits,
   }
   bool bad = false;
   int turn = 0;
-  for (int t = blockIdx.x * kGroups + group; t < a.T; t += gridDim.x * kGroups, turn ^= 1) {
-    // the losses' part: p and a of this thread's experts
-    float p[kEpt], c[kEpt], zt = 0.f;
-#pragma unroll
-    for (int i = 0; i < kEpt; ++i) p[i] = c[i] = 0.f;
-    float s[kMaxK + 1];
-#pragma unroll
-    for (int j = 0; j <= kMaxK; ++j) s[j] = 0.f;
+  for (; t < a.T; t += step, turn ^= 1) {
+    int my_row = next_row;
+    next_row = row_of(t + step);
+    // what the end of the token needs, on its way while the rows are read
+    float x[kEpt], l = 0.f, g = 0.f;
+    int id = -1;
+    bool on = false;
     if (dloss) {
-      int seq = 0;
-      bool on = !mask || mask[t];
-      if (off) {
-        int lo = 0, hi = a.n_seq - 1;  // the last sequence that begins at or before t
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (off[mid] <= t) lo = mid;
-          else hi = mid - 1;
-        }
-        seq = lo;
-        on = on && t >= off[seq] && t < off[seq + 1];
-      }
-      if (on) {
-        const float l = lse[t], n_s = (float)seq_info[seq];
-        const float scale = b / (n_s * n_s);
-        zt = z * l;
+      on = !mask || mask[t];
+      l = lse[t];
 #pragma unroll
-        for (int i = 0; i < kEpt; ++i) {
-          const int e = tid + i * 32 * W;
-          if (e < a.E) {
-            p[i] = expf(logits[(long long)t * a.E + e] - l);
-            c[i] = scale * (float)counts[(long long)seq * a.E + e];
-            s[kMaxK] = fmaf(p[i], c[i], s[kMaxK]);
-          }
-        }
+      for (int i = 0; i < kEpt; ++i) {
+        const int e = tid + i * 32 * W;
+        x[i] = e < a.E ? __ldg(logits + (long long)t * a.E + e) : 0.f;
       }
     }
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (dy) {
+      if (lane < a.k) {
+        g = __ldg(gates + (long long)t * a.k + lane);
+        id = __ldg(ids + (long long)t * a.k + lane);
+        if (id < 0 || id >= a.E) bad = true;
+        if (my_row < 0 || my_row >= a.r_max) {
+          bad = true;
+          my_row = -1;
+        }
+      } else {
+        my_row = -1;
+      }
       int row[kMaxK];
 #pragma unroll
-      for (int j = 0; j < kMaxK; ++j) {
-        row[j] = j < a.k ? __ldg(tok_row + (long long)t * a.k + j) : -1;
-        if (j < a.k && (row[j] < 0 || row[j] >= a.r_max)) {
-          bad = true;
-          row[j] = -1;
-        }
-      }
+      for (int j = 0; j < kMaxK; ++j) row[j] = __shfl_sync(0xffffffffu, my_row, j);
       for (int v = tid; v < a.d8; v += 32 * W) {
         uint4 r[kMaxK];
 #pragma unroll
@@ -117,40 +114,64 @@ router_backward_kernel(const RouterArgs a, const float* __restrict__ logits,
         }
       }
     }
+    // the losses' part: p and a of this thread's experts
+    float p[kEpt], c[kEpt], dot = 0.f;
 #pragma unroll
-    for (int j = 0; j <= kMaxK; ++j) s[j] = warp_sum(s[j]);
+    for (int i = 0; i < kEpt; ++i) p[i] = c[i] = 0.f;
+    if (on) {
+      int seq = 0;
+      if (off) {
+        int hi = a.n_seq - 1;  // the last sequence that begins at or before t
+        while (seq < hi) {
+          const int mid = (seq + hi + 1) >> 1;
+          if (off[mid] <= t) seq = mid;
+          else hi = mid - 1;
+        }
+        on = t >= off[seq] && t < off[seq + 1];
+      }
+      if (on) {
+        const float n_s = (float)seq_info[seq];
+        const float scale = b / (n_s * n_s);
+#pragma unroll
+        for (int i = 0; i < kEpt; ++i) {
+          const int e = tid + i * 32 * W;
+          if (e < a.E) {
+            p[i] = expf(x[i] - l);
+            c[i] = scale * (float)counts[(long long)seq * a.E + e];
+            dot = fmaf(p[i], c[i], dot);
+          }
+        }
+      }
+    }
+    dot = warp_sum(dot);
+    float sum = warp_sum8(s, lane);  // lane l: product l / 4
     if (W > 1) {
-      if (lane == 0) {
-#pragma unroll
-        for (int j = 0; j <= kMaxK; ++j) red[group][turn][j][warp] = s[j];
-      }
+      if ((lane & 3) == 0) red[group][turn][lane >> 2][warp] = sum;
+      if (lane == 0) red[group][turn][kMaxK][warp] = dot;
       asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(W * 32) : "memory");
+      sum = dot = 0.f;
 #pragma unroll
-      for (int j = 0; j <= kMaxK; ++j) {
-        s[j] = 0.f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) s[j] += red[group][turn][j][w];
+      for (int w = 0; w < W; ++w) {
+        dot += red[group][turn][kMaxK][w];
+        if (lane < kMaxK) sum += red[group][turn][lane][w];
       }
+    } else {
+      sum = __shfl_sync(0xffffffffu, sum, (lane * 4) & 31);  // lane j: product j
     }
     float out[kEpt];
 #pragma unroll
-    for (int i = 0; i < kEpt; ++i) out[i] = p[i] * (c[i] - s[kMaxK] + zt);
+    for (int i = 0; i < kEpt; ++i) out[i] = p[i] * (c[i] - dot + z * l);
     if (dy) {
-      float g[kMaxK], mean = 0.f;
+      const float mean = warp_sum(lane < a.k ? g * sum : 0.f);
+      const float add = g * (sum - mean);
+      if (dgates && warp == 0 && lane < a.k) dgates[(long long)t * a.k + lane] = sum;
 #pragma unroll
       for (int j = 0; j < kMaxK; ++j) {
-        g[j] = j < a.k ? __ldg(gates + (long long)t * a.k + j) : 0.f;
-        mean = fmaf(g[j], s[j], mean);
-      }
-#pragma unroll
-      for (int j = 0; j < kMaxK; ++j) {
-        if (j >= a.k) break;
-        const int e = __ldg(ids + (long long)t * a.k + j);
-        if (e < 0 || e >= a.E) bad = true;
+        const int e = __shfl_sync(0xffffffffu, id, j);
+        const float to = __shfl_sync(0xffffffffu, add, j);
 #pragma unroll
         for (int i = 0; i < kEpt; ++i)
-          if (e == tid + i * 32 * W) out[i] = fmaf(g[j], s[j] - mean, out[i]);
-        if (dgates && tid == j) dgates[(long long)t * a.k + j] = s[j];
+          if (e == tid + i * 32 * W) out[i] += to;
       }
     }
 #pragma unroll
@@ -187,9 +208,28 @@ cudaError_t launch_router_backward(const moe_cfg& c, const float* logits, const 
         counts, seq_info, lse, dloss, dgates, dlogits, status);
     return cudaGetLastError();
   };
-  if (a.d8 <= 64) return run(router_backward_kernel<1>, 1);
-  if (a.d8 <= 256) return run(router_backward_kernel<4>, 4);
-  return run(router_backward_kernel<8>, 8);
+  auto warps = [&](auto w) {
+    constexpr int W = decltype(w)::value;
+    const int ept = (c.E + 32 * W - 1) / (32 * W);
+    if constexpr (W <= 1)
+      if (ept > 4) return run(router_backward_kernel<W, 8>, W);
+    if constexpr (W <= 2)
+      if (ept > 2) return run(router_backward_kernel<W, 4>, W);
+    if constexpr (W <= 2)
+      if (ept > 1) return run(router_backward_kernel<W, 2>, W);
+    return run(router_backward_kernel<W, 1>, W);
+  };
+  // Warps a token, by the 16-byte loads that a token is (k rows of O, twice that of dy) and
+  // the tokens there are.  Measured us, 1 | 2 | 8 warps a token: 16384 tokens of 8 x 2048
+  // (2560 loads) 149 | 141 | 119, 1 token of 8 x 7168 37 | 10 | 5; below that the end of a token
+  // costs more than its rows, and fewer warps share it: 16384 of 4 x 512 28 | 31 | 74, of
+  // 2 x 4096 97 | 96 | 130, but with few tokens a second warp still finds an idle SM: 2048 of
+  // 4 x 1024 10.3 | 7.4 | 11.7, 1111 of 4 x 512 4.2 | 3.7 | 6.7.
+  const int loads = a.d8 * (c.k + 2);
+  if (loads >= 2560 || (loads && c.T < num_sms()))
+    return warps(std::integral_constant<int, 8>());
+  if (c.T < num_sms() * 32) return warps(std::integral_constant<int, 2>());
+  return warps(std::integral_constant<int, 1>());
 }
 
 }  // namespace moe

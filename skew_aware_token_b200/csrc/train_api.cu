@@ -147,8 +147,14 @@ int moet_adamw_step(const moet_adamw_tensor* tensors, int32_t count, const moet_
     if (t.n > kMaxTensor) return MOE_ERR_UNSUPPORTED;
     if (t.n == 0) continue;
     rc = check_ptrs({t.p, t.g, t.m, t.v});
-    if (rc == MOE_OK && t.state_dtype == MOET_E4M3) rc = check_ptrs({t.m_scale, t.v_scale});
-    else if (rc == MOE_OK && (t.m_scale || t.v_scale)) rc = MOE_ERR_INVALID_ARG;
+    if (rc == MOE_OK && (t.state_dtype == MOET_E4M3) != (t.m_scale && t.v_scale))
+      rc = MOE_ERR_INVALID_ARG;
+    if (rc == MOE_OK && t.state_dtype == MOET_F32 && (t.m_scale || t.v_scale))
+      rc = MOE_ERR_INVALID_ARG;
+    // the scales are read one at a time
+    if (rc == MOE_OK && ((reinterpret_cast<uintptr_t>(t.m_scale) |
+                          reinterpret_cast<uintptr_t>(t.v_scale)) & 3u))
+      rc = MOE_ERR_UNSUPPORTED;
     if (rc == MOE_OK) rc = check_optional({t.master});
   }
   if (rc != MOE_OK) return rc;

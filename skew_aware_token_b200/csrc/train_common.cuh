@@ -80,6 +80,48 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// ---- a thread's own copies ahead of time: 16 bytes from global to its shared-memory slots,
+// read back by the same thread after wait_copies() (so no barrier guards them) ----
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void copy_ahead16(uint32_t dst, const void* src) {
+  // through L1: the second half of a 32-byte sector that two copies share hits there
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void commit_copies() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+__device__ __forceinline__ uint4 slot16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+// Sums of up to 8 values over the warp with 9 shuffles: each of the first three exchanges
+// halves the number of values a lane still carries.  Lane l returns the sum of value l / 4.
+__device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
+#pragma unroll
+  for (int half = 4; half >= 1; half >>= 1) {
+    const int off = half * 4;
+    const bool up = lane & off;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float send = up ? v[i] : v[i + half], keep = up ? v[i + half] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+    }
+  }
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
 // ---- launches that overlap their predecessor's end (programmatic dependent launch) ----
 // The dependent kernel calls wait_for_predecessor() before it touches what the kernels
 // before it wrote; that returns once the predecessor has ended and its writes are visible.

@@ -23,13 +23,17 @@ from __future__ import annotations
 
 import collections
 import ctypes
+import operator
 
+import numpy as np
 import torch
 
 from . import native as N
 
 _TYPES = {torch.float32: N.MOET_F32, torch.bfloat16: N.MOET_BF16,
           torch.float8_e4m3fn: N.MOET_E4M3}
+_GRAD_TYPES = {torch.float32, torch.bfloat16}
+_dtype_of = operator.attrgetter("dtype")
 
 
 def _device(device) -> torch.device:
@@ -40,19 +44,21 @@ def _device(device) -> torch.device:
 
 
 def _need(t, name, dtype, n, dev, optional=False):
-    """Checks one array argument: a contiguous tensor of `dtype` on `dev` with `n` elements,
-    or a flat buffer of at least that many (what MoeLayer owns)."""
+    """The address of one array argument, after its checks: a contiguous tensor of `dtype` on
+    `dev` with `n` elements, or a flat buffer of at least that many (what MoeLayer owns).
+    None when it is left out."""
     if t is None:
         if optional:
-            return
+            return None
         raise TypeError(f"{name} is needed")
-    if not isinstance(t, torch.Tensor) or t.device != dev:
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev.index:
         raise TypeError(f"{name} must be a tensor on {dev}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     have = t.numel()
     if not t.is_contiguous() or (have != n and (have < n or t.dim() != 1)):
         raise ValueError(f"{name} must be contiguous with {n} elements")
+    return t.data_ptr()
 
 
 class _OnDevice:
@@ -62,9 +68,8 @@ class _OnDevice:
         dev = self.device
         if stream is None:
             stream = torch.cuda.current_stream(dev).cuda_stream
-        elif isinstance(stream, torch.cuda.Stream):
-            if stream.device != dev:
-                raise ValueError(f"the stream is on {stream.device}, the arrays on {dev}")
+        elif isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the arrays on {dev}")
         if torch.cuda.current_device() == dev.index:
             fn(*args, stream=stream)
         else:
@@ -95,25 +100,31 @@ class RouterLoss(_OnDevice):
         self.dlogits = self._dlogits[:T * E].view(T, E)
         self.workspace = z(size, dt=torch.uint8)
         self.status = z(4, dt=torch.int32)
+        self._rows = N.moe_workspace_size(self.cfg, N.MOE_WS_ROWS)
+        # the addresses of the buffers above, in the entry points' order
+        self._outputs = [t.data_ptr() for t in (self.losses, self.counts, self.probs,
+                                                self.seq_info, self._lse, self.workspace,
+                                                self.status)]
+        self._saved = [t.data_ptr() for t in (self.counts, self.seq_info, self._lse)]
+        self._grads = [t.data_ptr() for t in (self._dgates, self._dlogits, self.status)]
 
-    def _check_batch(self, token_mask, seq_off):
-        _need(token_mask, "token_mask", torch.uint8, self.cfg.T, self.device, optional=True)
-        _need(seq_off, "seq_off", torch.int32, self.n_seq + 1, self.device,
-              optional=self.n_seq == 1)
+    def _batch(self, token_mask, seq_off):
+        return (_need(token_mask, "token_mask", torch.uint8, self.cfg.T, self.device, True),
+                _need(seq_off, "seq_off", torch.int32, self.n_seq + 1, self.device,
+                      self.n_seq == 1))
 
     def __call__(self, logits, topk_ids, token_mask=None, seq_off=None, stream=None):
         """fp32 [2]: balance loss and z loss of logits fp32 [T, E] and the router's topk_ids
         int32 [T, k].  token_mask uint8 [T] leaves tokens out; seq_off int32 [n_seq + 1] are
         the sequences' bounds (None with one sequence: the whole batch)."""
         c, dev = self.cfg, self.device
-        _need(logits, "logits", torch.float32, c.T * c.E, dev)
-        _need(topk_ids, "topk_ids", torch.int32, c.T * c.k, dev)
-        self._check_batch(token_mask, seq_off)
-        if c.T == 0:
-            logits, topk_ids, token_mask = self._dlogits, self._dlogits, None
-        self._call(N.moet_balance_loss, c, logits, topk_ids, token_mask, seq_off, self.n_seq,
-                   self.losses, self.counts, self.probs, self.seq_info, self._lse,
-                   self.workspace, self.status, stream=stream)
+        x = _need(logits, "logits", torch.float32, c.T * c.E, dev)
+        ids = _need(topk_ids, "topk_ids", torch.int32, c.T * c.k, dev)
+        mask, off = self._batch(token_mask, seq_off)
+        if c.T == 0:  # empty tensors have no address
+            x, ids, mask = self._grads[1], self._grads[1], None
+        self._call(N.moet_balance_loss, c, x, ids, mask, off, self.n_seq, *self._outputs,
+                   stream=stream)
         return self.losses
 
     def backward(self, logits=None, topk_ids=None, topk_gates=None, dloss=None, dy=None, o=None,
@@ -126,23 +137,22 @@ class RouterLoss(_OnDevice):
         gates = dy is not None or o is not None or tok_row is not None
         if not gates and dloss is None:
             raise ValueError("nothing to take the gradient of: give dloss, or dy, o and tok_row")
+        x = ids = g = dy_p = o_p = row = mask = off = dl = None
         if gates:
-            rows = N.moe_workspace_size(c, N.MOE_WS_ROWS)
-            _need(topk_ids, "topk_ids", torch.int32, c.T * c.k, dev)
-            _need(topk_gates, "topk_gates", torch.float32, c.T * c.k, dev)
-            _need(dy, "dy", torch.float32, c.T * c.d, dev)
-            _need(o, "o", torch.bfloat16, rows * c.d, dev)
-            _need(tok_row, "tok_row", torch.int32, c.T * c.k, dev)
+            ids = _need(topk_ids, "topk_ids", torch.int32, c.T * c.k, dev)
+            g = _need(topk_gates, "topk_gates", torch.float32, c.T * c.k, dev)
+            dy_p = _need(dy, "dy", torch.float32, c.T * c.d, dev)
+            o_p = _need(o, "o", torch.bfloat16, self._rows * c.d, dev)
+            row = _need(tok_row, "tok_row", torch.int32, c.T * c.k, dev)
         if dloss is not None:
-            _need(dloss, "dloss", torch.float32, 2, dev)
-            _need(logits, "logits", torch.float32, c.T * c.E, dev)
-            self._check_batch(token_mask, seq_off)
+            dl = _need(dloss, "dloss", torch.float32, 2, dev)
+            x = _need(logits, "logits", torch.float32, c.T * c.E, dev)
+            mask, off = self._batch(token_mask, seq_off)
         if c.T == 0:
             return self.dlogits
-        self._call(N.moet_router_backward, c, logits, topk_ids, topk_gates, dy, o, tok_row,
-                   token_mask, seq_off, self.n_seq, self.counts, self.seq_info, self._lse,
-                   dloss, self._dgates if gates else None, self._dlogits, self.status,
-                   stream=stream)
+        dgates, dlogits, status = self._grads
+        self._call(N.moet_router_backward, c, x, ids, g, dy_p, o_p, row, mask, off, self.n_seq,
+                   *self._saved, dl, dgates if gates else None, dlogits, status, stream=stream)
         return self.dlogits
 
     def clear_status(self):
@@ -190,35 +200,35 @@ class BlockNorm(_OnDevice):
             self.dw_post, self.dw_next = new(torch.float32, d), new(torch.float32, d)
             self.workspace = new(torch.uint8, size)
 
-    def _check(self, h, y, gate, w_post, w_next):
+    def _inputs(self, h, y, gate, w_post, w_next):
         T, d, dev = self.cfg.T, self.cfg.d, self.device
-        _need(h, "h", self.h_dtype, T * d, dev)
-        _need(y, "y", torch.float32, T * d, dev, optional=True)
-        _need(gate, "gate", torch.float32, T, dev, optional=True)
-        _need(w_post, "w_post", self.w_dtype, d, dev, optional=True)
-        _need(w_next, "w_next", self.w_dtype, d, dev, optional=True)
         if y is None and (gate is not None or w_post is not None):
             raise ValueError("gate and w_post belong to y")
+        return (_need(h, "h", self.h_dtype, T * d, dev),
+                _need(y, "y", torch.float32, T * d, dev, True),
+                _need(gate, "gate", torch.float32, T, dev, True),
+                _need(w_post, "w_post", self.w_dtype, d, dev, True),
+                _need(w_next, "w_next", self.w_dtype, d, dev, True))
 
     def __call__(self, h, y=None, gate=None, w_post=None, w_next=None, h_out=None, stream=None):
         """(h_out, x): the residual stream behind the block and, with w_next, the next
         block's bf16 rows.  Without y, h_out is h itself (a norm before the first block).
         `h_out=` takes the result's place in the caller's buffer; it may be h itself."""
         c = self.cfg
-        self._check(h, y, gate, w_post, w_next)
+        inputs = self._inputs(h, y, gate, w_post, w_next)
         if y is None and w_next is None:
             raise ValueError("nothing to compute: give y, w_next or both")
         if y is None:
             if h_out is not None:
                 raise ValueError("h_out is written only with y")
-        elif h_out is None:
-            h_out = self.h_out
+            to = None
         else:
-            _need(h_out, "h_out", self.h_dtype, c.T * c.d, self.device)
+            h_out = self.h_out if h_out is None else h_out
+            to = _need(h_out, "h_out", self.h_dtype, c.T * c.d, self.device)
         x = None if w_next is None else self.x
         if c.T:
-            self._call(N.moet_block_norm, c, self.norm, h, y, gate, w_post, w_next, h_out, x,
-                       stream=stream)
+            self._call(N.moet_block_norm, c, self.norm, *inputs, to,
+                       None if x is None else x.data_ptr(), stream=stream)
         return (h if y is None else h_out), x
 
     def backward(self, h_out, y=None, gate=None, w_post=None, w_next=None, dh_out=None, dx=None,
@@ -230,9 +240,9 @@ class BlockNorm(_OnDevice):
             raise ValueError("built without train=True")
         c = self.cfg
         T, d, dev = c.T, c.d, self.device
-        self._check(h_out, y, gate, w_post, w_next)
-        _need(dh_out, "dh_out", self.h_dtype, T * d, dev, optional=True)
-        _need(dx, "dx", torch.float32, T * d, dev, optional=True)
+        inputs = self._inputs(h_out, y, gate, w_post, w_next)
+        into = (_need(dh_out, "dh_out", self.h_dtype, T * d, dev, True),
+                _need(dx, "dx", torch.float32, T * d, dev, True))
         if (w_next is None) != (dx is None):
             raise ValueError("dx and w_next are given together")
         if dh_out is None and dx is None:
@@ -241,9 +251,9 @@ class BlockNorm(_OnDevice):
         g = BlockNormGrads(self.dh, only(self.dy, y), only(self.dgate, gate),
                            only(self.dw_post, w_post), only(self.dw_next, w_next))
         if T:
-            self._call(N.moet_block_norm_backward, c, self.norm, h_out, y, gate, w_post, w_next,
-                       dh_out, dx, g.dh, g.dy, g.dgate, g.dw_post, g.dw_next, self.workspace,
-                       stream=stream)
+            self._call(N.moet_block_norm_backward, c, self.norm, *inputs, *into,
+                       *[None if t is None else t.data_ptr() for t in g],
+                       self.workspace.data_ptr(), stream=stream)
         else:
             for dw in (g.dw_post, g.dw_next):
                 if dw is not None:
@@ -335,6 +345,13 @@ class AdamW(_OnDevice):
             if begin < end:
                 raise ValueError(f"{a} and {b} share memory")
         self._sizes = sizes
+        # the descriptors' fields that a step fills in, as arrays over the tensors
+        at = {n: getattr(N.MoetAdamwTensor, n).offset for n in ("g", "g_dtype")}
+        fields = np.frombuffer(self._tensors, dtype=np.dtype(
+            {"names": list(at), "formats": [np.uint64, np.int32], "offsets": list(at.values()),
+             "itemsize": ctypes.sizeof(N.MoetAdamwTensor)}))
+        self._g, self._g_dtype = fields["g"], fields["g_dtype"]
+        self._devices = [dev.index] * count
         self._opt = N.MoetAdamw(float(betas[0]), float(betas[1]), float(eps))
         self.lr = torch.full((4,), float(lr), device=dev)
         self.steps = torch.tensor([step, 0, 0, 0], dtype=torch.int32, device=dev)
@@ -350,13 +367,19 @@ class AdamW(_OnDevice):
         grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
-        dev = self.device
-        for i, (e, g, n) in enumerate(zip(self._tensors, grads, self._sizes)):
-            t = _TYPES.get(g.dtype) if isinstance(g, torch.Tensor) else None
-            if t is None or t == N.MOET_E4M3:
-                raise TypeError(f"grads[{i}] must be a torch.float32 or torch.bfloat16 tensor")
-            _need(g, f"grads[{i}]", g.dtype, n, dev)
-            e.g, e.g_dtype = g.data_ptr(), t
-        _need(grad_scale, "grad_scale", torch.float32, 1, dev, optional=True)
-        self._call(N.moet_adamw_step, self._tensors, len(grads), self._opt, self.lr, grad_scale,
+        # over all of them at once: a loop over hundreds of tensors costs more than the step
+        if not all(isinstance(g, torch.Tensor) for g in grads):
+            raise TypeError("grads must be tensors")
+        types = list(map(_dtype_of, grads))
+        if not _GRAD_TYPES.issuperset(types):
+            raise TypeError("grads must be torch.float32 or torch.bfloat16 tensors")
+        if list(map(torch.Tensor.get_device, grads)) != self._devices:
+            raise TypeError(f"grads must be on {self.device}")
+        if list(map(torch.Tensor.numel, grads)) != self._sizes or \
+                not all(map(torch.Tensor.is_contiguous, grads)):
+            raise ValueError("grads must be contiguous and of their parameters' sizes")
+        self._g[:] = list(map(torch.Tensor.data_ptr, grads))
+        self._g_dtype[:] = list(map(_TYPES.__getitem__, types))
+        scale = _need(grad_scale, "grad_scale", torch.float32, 1, self.device, True)
+        self._call(N.moet_adamw_step, self._tensors, len(grads), self._opt, self.lr, scale,
                    self.steps, stream=stream)

@@ -515,6 +515,34 @@ def test_adamw_scale_skip_and_mixed_tensors():
                                                        else 0), f"p[{i}]")
 
 
+def test_adamw_on_views_of_flat_storage():
+    """Tensors that are views into one buffer each (scales on 4 bytes), odd ends: the result
+    of tensors of their own, and nothing between the views written."""
+    sizes, starts = [1, 300, 1000, 5], [0, 256, 768, 2048]
+    ps, gs = adam_inputs(sizes, torch.bfloat16, torch.float32, seed=3)
+    flat = dict(p=torch.full((2304,), 7, dtype=torch.bfloat16, device=DEV),
+                m=torch.zeros(2304, device=DEV).to(torch.float8_e4m3fn),
+                v=torch.zeros(2304, device=DEV).to(torch.float8_e4m3fn),
+                ms=torch.zeros(9, device=DEV), vs=torch.zeros(9, device=DEV))
+    cut = lambda x: [x[a:a + n] for a, n in zip(starts, sizes)]
+    scale = lambda x: [x[a // 256:a // 256 + -(-n // 256)] for a, n in zip(starts, sizes)]
+    for view, p in zip(cut(flat["p"]), ps):
+        view.copy_(p)
+    opt = AdamW(cut(flat["p"]), state_bits=8, m=cut(flat["m"]), v=cut(flat["v"]),
+                m_scale=scale(flat["ms"]), v_scale=scale(flat["vs"]))
+    alone = AdamW([p.to(DEV) for p in ps], state_bits=8)
+    for _ in range(2):
+        opt.step([g.to(DEV) for g in gs])
+        alone.step([g.to(DEV) for g in gs])
+    for name in ("params", "m", "v", "m_scale", "v_scale"):
+        for a, b in zip(getattr(opt, name), getattr(alone, name)):
+            assert torch.equal(a.float(), b.float()), name
+    gap = torch.ones(2304, dtype=torch.bool)
+    for a, n in zip(starts, sizes):
+        gap[a:a + n] = False
+    assert bool((flat["p"].cpu()[gap] == 7).all()) and not flat["m"].float().cpu()[gap].any()
+
+
 def test_adamw_bad_gradients_stay_in_their_block():
     n = 1024
     for bits in (32, 8):

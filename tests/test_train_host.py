@@ -167,6 +167,9 @@ def test_adamw_refusals():
     assert go(tensors(master=OK + 2, p_dtype=1)) == UNSUPPORTED
     assert go(tensors(m_scale=OK, v_scale=OK)) == INVALID
     assert go(tensors(state_dtype=2)) == INVALID         # 8-bit states without scales
+    assert go(tensors(state_dtype=2, m_scale=OK)) == INVALID
+    assert go(tensors(v_scale=OK)) == INVALID
+    assert go(tensors(state_dtype=2, m_scale=OK + 2, v_scale=OK)) == UNSUPPORTED
     for bad in (dict(n=-1), dict(p_dtype=2), dict(g_dtype=2), dict(g_dtype=-1),
                 dict(state_dtype=1), dict(weight_decay=float("nan"))):
         assert go(tensors(**bad)) == INVALID, bad
