@@ -63,16 +63,29 @@ struct Consts {
   float b1, b2, omb1, omb2, log_b1, log_b2, eps, one;
 };
 
+__device__ __forceinline__ float2 bf16_pair(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ void decode8(uint32_t lo, uint32_t hi, float2 (&v)[4]) {
+  const uint32_t w[2] = {lo, hi};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+        (__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i % 2))), __NV_E4M3);
+    v[i] = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  }
+}
+
 // A lane's 8 elements of a block, as 4 pairs.  With 8-bit states they are consecutive (one
 // load of 8 codes, one or two of the rest); with fp32 states two runs of 4, one in either
 // half of the block, so that the loads of 16 bytes stay consecutive over the lanes.
 // FULL: the whole block lies inside the tensor.
 template <bool S8>
 struct Lane {
-  long long at, n;  // the first element, the tensor's length
-  __device__ Lane(long long block, int lane, long long n)
-      : at(block * kBlock + lane * (S8 ? 8 : 4)), n(n) {}
-  __device__ long long index(int i) const { return at + (S8 || i < 4 ? i : kBlock / 2 + i - 4); }
+  uint32_t at, n;  // the lane's first element, and the elements there are, from the tile's first
+  __device__ Lane(int warp, int lane, uint32_t n)
+      : at(warp * kBlock + lane * (S8 ? 8 : 4)), n(n) {}
+  __device__ uint32_t index(int i) const { return at + (S8 || i < 4 ? i : kBlock / 2 + i - 4); }
 
   template <bool FULL>
   __device__ void load(const float* p, float2 (&v)[4]) const {
@@ -101,8 +114,7 @@ struct Lane {
       }
       const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+      for (int i = 0; i < 4; ++i) v[i] = bf16_pair(w[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -122,12 +134,7 @@ struct Lane {
       for (int i = 0; i < 8; ++i)
         if (index(i) < n) w[i / 4] |= (uint32_t)p[index(i)] << (8 * (i % 4));
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-          (__nv_fp8x2_storage_t)(w[i / 2] >> (16 * (i % 2))), __NV_E4M3);
-      v[i] = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    }
+    decode8(w[0], w[1], v);
   }
   template <bool FULL>
   __device__ void store(float* p, const float2 (&v)[4]) const {
@@ -188,6 +195,16 @@ __device__ __forceinline__ float top3(float a, float b, float c) {
 __device__ __forceinline__ float warp_top(float v) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
+__device__ __forceinline__ float least3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float near_root(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float reciprocal(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -217,108 +234,260 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return pair(r);
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 mulc(float2 a, float c) { return mul2(a, both(c)); }
+// The sum of two rounded products, as a * one + b with a `one` that the compiler cannot see:
+// it fuses a packed product and sum (even with .rn) into one rounding.
+__device__ __forceinline__ float2 sum2(float2 a, float2 b, const Consts& c) {
+  return fma2(a, both(c.one), b);
+}
 
 struct Step {
   float gs, lr, lr1, inv2;  // gradient scale, lr, lr / (1 - b1^t), (1 - b2^t)^-1/2
   bool scaled;
 };
 
-// One block of one tensor by one warp.
-template <int W, bool GBF16, bool S8, bool FULL>
-__device__ __forceinline__ void update_block(const Item& it, long long block, int lane,
-                                             const Consts& c, const Step& st) {
+// A lane's values of a block before the step.
+struct Values {
+  float2 g[4], p[4], m[4], v[4];
+  float sm, sv;  // scales of an 8-bit block
+};
+
+template <int W, bool GBF16, bool S8>
+struct Types {
   using G = typename std::conditional<GBF16, __nv_bfloat16, float>::type;
   using P = typename std::conditional<W == W_F32, float, __nv_bfloat16>::type;
   using M = typename std::conditional<S8, uint8_t, float>::type;
-  const Lane<S8> at(block, lane, it.n);
-  float2 g[4], p[4], m[4], v[4];
-  at.template load<FULL>(static_cast<const G*>(it.g), g);
-  if constexpr (W == W_BF16_MASTER) at.template load<FULL>(it.master, p);
-  else at.template load<FULL>(static_cast<const P*>(it.p), p);
-  at.template load<FULL>(static_cast<const M*>(it.m), m);
-  at.template load<FULL>(static_cast<const M*>(it.v), v);
-  float sm = 0.f, sv = 0.f;
-  if constexpr (S8) {
-    sm = it.m_scale[block];
-    sv = it.v_scale[block];
-  }
-  const float2 decay = both(fmaf(-st.lr, it.wd, 1.f)), by = both(-st.lr1);
-  float2 r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  using Source = typename std::conditional<W == W_BF16, __nv_bfloat16, float>::type;
+};
+
+// One tile's part of a tensor: the addresses of its first element.  They are the same for
+// the whole CTA, and a lane's place in the tile is 32 bits that stay, so that the accesses
+// need no address arithmetic of the lanes.
+template <int W, bool GBF16, bool S8>
+struct Tile {
+  using T = Types<W, GBF16, S8>;
+  const typename T::G* g;
+  typename T::P* p;
+  float* master;
+  typename T::M* m;
+  typename T::M* v;
+  float* m_scale;
+  float* v_scale;
+  float wd;
+  uint32_t n;  // elements from here to the tensor's end, at most kTile (0: no tile)
+  template <int CAP>
+  __device__ Tile(const Batch<CAP>& b, int item, int tile) {
+    n = 0;
+    if (item >= b.count) return;
+    const Item& it = b.item[item];
+    const long long in = tile - b.first_tile[item], first = in * kTile;
+    g = static_cast<const typename T::G*>(it.g) + first;
+    p = static_cast<typename T::P*>(it.p) + first;
+    if constexpr (W == W_BF16_MASTER) master = it.master + first;
+    m = static_cast<typename T::M*>(it.m) + first;
+    v = static_cast<typename T::M*>(it.v) + first;
     if constexpr (S8) {
-      m[i] = mul2(m[i], both(sm));
-      v[i] = mul2(v[i], both(sv));
-      v[i] = mul2(v[i], v[i]);
+      m_scale = it.m_scale + in * (kThreads / 32);
+      v_scale = it.v_scale + in * (kThreads / 32);
     }
-    if (st.scaled) g[i] = mul2(g[i], both(st.gs));
-    // Sums of two rounded products: as a * one + b with a `one` that the compiler cannot see,
-    // since it fuses a packed product and sum (even with .rn) into one rounding.
-    m[i] = fma2(mul2(m[i], both(c.b1)), both(c.one), mul2(g[i], both(c.omb1)));
-    v[i] = fma2(mul2(v[i], both(c.b2)), both(c.one), mul2(mul2(g[i], both(c.omb2)), g[i]));
-    r[i] = make_float2(__fsqrt_rn(v[i].x), __fsqrt_rn(v[i].y));
-    const float2 den = fma2(r[i], both(st.inv2), both(c.eps));
-    const float2 q = mul2(m[i], make_float2(reciprocal(den.x), reciprocal(den.y)));
-    p[i] = fma2(by, q, mul2(p[i], decay));
+    wd = it.wd;
+    n = (uint32_t)(it.n - first < kTile ? it.n - first : kTile);
   }
-  at.template store<FULL>(static_cast<P*>(it.p), p);
-  if constexpr (W == W_BF16_MASTER) at.template store<FULL>(it.master, p);
+  __device__ const typename T::Source* weights() const {
+    if constexpr (W == W_BF16_MASTER) return master;
+    else return p;
+  }
+};
+
+template <int W, bool GBF16, bool S8, bool FULL>
+__device__ __forceinline__ void load_values(const Tile<W, GBF16, S8>& tl, int warp, int lane,
+                                            Values& x) {
+  const Lane<S8> at(warp, lane, tl.n);
+  at.template load<FULL>(tl.g, x.g);
+  at.template load<FULL>(tl.weights(), x.p);
+  at.template load<FULL>(tl.m, x.m);
+  at.template load<FULL>(tl.v, x.v);
   if constexpr (S8) {
-    float top_m = 0.f, top_r = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      top_m = top3(m[i].x, m[i].y, top_m);
-      top_r = top3(r[i].x, r[i].y, top_r);
-    }
-    top_m = warp_top(top_m);
-    top_r = warp_top(top_r);
-    const bool some_m = !(top_m < kLeastTop), some_r = !(top_r < kLeastTop);
-    const float im = some_m ? __fmul_rn(kE4m3Max, __frcp_rn(top_m)) : 0.f;
-    const float ir = some_r ? __fmul_rn(kE4m3Max, __frcp_rn(top_r)) : 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      m[i] = mul2(m[i], both(im));
-      // a positive root is 2^-75 and more: min(r * 1e38, tiny) is tiny for it, 0 for 0
-      const float2 least = mul2(r[i], both(1e38f));
-      v[i] = mul2(r[i], both(ir));
-      v[i].x = fmaxf(v[i].x, fminf(least.x, kE4m3Tiny));
-      v[i].y = fmaxf(v[i].y, fminf(least.y, kE4m3Tiny));
-    }
-    if (lane == 0) {
-      it.m_scale[block] = some_m ? __fmul_rn(top_m, 1.f / kE4m3Max) : 0.f;
-      it.v_scale[block] = some_r ? __fmul_rn(top_r, 1.f / kE4m3Max) : 0.f;
-    }
+    x.sm = tl.m_scale[warp];
+    x.sv = tl.v_scale[warp];
   }
-  at.template store<FULL>(static_cast<M*>(it.m), m);
-  at.template store<FULL>(static_cast<M*>(it.v), v);
 }
 
+// One block of one tensor by one warp.
+template <int W, bool GBF16, bool S8, bool FULL>
+__device__ __forceinline__ void step_block(const Tile<W, GBF16, S8>& tl, int warp, int lane,
+                                           const Consts& c, const Step& st, Values& x) {
+  const Lane<S8> at(warp, lane, tl.n);
+  const float decay = fmaf(-st.lr, tl.wd, 1.f), by = -st.lr1;
+  float2 r[4];  // the root to 2^-23 of itself, as the weights need it
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 m = x.m[i], v = x.v[i], g = x.g[i];
+    if constexpr (S8) {
+      m = mulc(m, x.sm);
+      v = mulc(v, x.sv);
+      v = mul2(v, v);
+    }
+    if (st.scaled) g = mulc(g, st.gs);
+    m = sum2(mulc(m, c.b1), mulc(g, c.omb1), c);
+    v = sum2(mulc(v, c.b2), mul2(mulc(g, c.omb2), g), c);
+    r[i] = make_float2(near_root(v.x), near_root(v.y));
+    const float2 den = fma2(r[i], both(st.inv2), both(c.eps));
+    const float2 q = mul2(m, make_float2(reciprocal(den.x), reciprocal(den.y)));
+    x.p[i] = fma2(q, both(by), mulc(x.p[i], decay));
+    x.m[i] = m;
+    x.v[i] = v;
+  }
+  at.template store<FULL>(tl.p, x.p);
+  if constexpr (W == W_BF16_MASTER) at.template store<FULL>(tl.master, x.p);
+  if constexpr (S8) {
+    float top_m = 0.f, top_v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      top_m = top3(x.m[i].x, x.m[i].y, top_m);
+      top_v = top3(x.v[i].x, x.v[i].y, top_v);
+    }
+    top_m = warp_top(top_m);
+    top_v = warp_top(top_v);  // the nearest root rises with v: the largest root is its
+    // even lanes take the codes' factor of m, odd ones of r: one root and reciprocal a lane
+    const float top = lane & 1 ? __fsqrt_rn(top_v) : top_m;
+    const bool some = !(top < kLeastTop);
+    const float inv = some ? __fmul_rn(kE4m3Max, __frcp_rn(top)) : 0.f;
+    const float im = __shfl_sync(0xffffffffu, inv, 0), ir = __shfl_sync(0xffffffffu, inv, 1);
+    uint32_t border = ~0u;
+    float least = INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x.m[i] = mulc(x.m[i], im);
+      r[i] = mulc(r[i], ir);
+      // The code goes by the nearest root.  This one, and its product, are off by 4 steps at
+      // most, which matters only next to a border between codes (half way in the last 20
+      // bits, above the subnormal codes): 8 steps from one, or below 2^-6, it is done again.
+      border = __vimin3_u32(border, (__float_as_uint(r[i].x) + 0x80008u) & 0xfffffu,
+                            (__float_as_uint(r[i].y) + 0x80008u) & 0xfffffu);
+      least = least3(r[i].x, r[i].y, least);
+    }
+    if ((border <= 16u || least < 0.015625f) && ir > 0.f) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        r[i] = make_float2(__fmul_rn(__fsqrt_rn(x.v[i].x), ir),
+                           __fmul_rn(__fsqrt_rn(x.v[i].y), ir));
+        if (x.v[i].x > 0.f) r[i].x = fmaxf(r[i].x, kE4m3Tiny);
+        if (x.v[i].y > 0.f) r[i].y = fmaxf(r[i].y, kE4m3Tiny);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.v[i] = r[i];
+    if (lane < 2)
+      (lane ? tl.v_scale : tl.m_scale)[warp] = some ? __fmul_rn(top, 1.f / kE4m3Max) : 0.f;
+  }
+  at.template store<FULL>(tl.m, x.m);
+  at.template store<FULL>(tl.v, x.v);
+}
+
+// 16-byte slots of a thread, kThreads apart: the next block's gradient, weights and codes.
+template <int W, bool GBF16>
+struct Ahead {
+  static constexpr int kG = GBF16 ? 1 : 2, kP = W == W_BF16 ? 1 : 2;
+  static constexpr int kPitch = 16 * kThreads, kBytes = (kG + kP + 1) * kPitch;
+  uint32_t slot;
+  float sm, sv;
+  __device__ explicit Ahead(const char* smem) : slot(smem_addr(smem) + threadIdx.x * 16) {}
+  __device__ void fill(const Tile<W, GBF16, true>& tl, int warp, int lane) {
+    const uint32_t at = warp * kBlock + lane * 8;
+    const char* g = reinterpret_cast<const char*>(tl.g + at);
+    const char* p = reinterpret_cast<const char*>(tl.weights() + at);
+#pragma unroll
+    for (int i = 0; i < kG; ++i) copy_ahead16(slot + i * kPitch, g + 16 * i);
+#pragma unroll
+    for (int i = 0; i < kP; ++i) copy_ahead16(slot + (kG + i) * kPitch, p + 16 * i);
+    copy_ahead8(slot + (kG + kP) * kPitch, tl.m + at);
+    copy_ahead8(slot + (kG + kP) * kPitch + 8, tl.v + at);
+    sm = tl.m_scale[warp];
+    sv = tl.v_scale[warp];
+  }
+  template <int UNITS>
+  __device__ void read(int unit, float2 (&v)[4]) const {
+    const uint4 a = slot16(slot + unit * kPitch);
+    if constexpr (UNITS == 1) {
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = bf16_pair(w[i]);
+    } else {
+      const uint4 b = slot16(slot + (unit + 1) * kPitch);
+      v[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+      v[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+      v[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
+      v[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+    }
+  }
+  __device__ void take(Values& x) const {
+    read<kG>(0, x.g);
+    read<kP>(kG, x.p);
+    const uint4 a = slot16(slot + (kG + kP) * kPitch);
+    decode8(a.x, a.y, x.m);
+    decode8(a.z, a.w, x.v);
+    x.sm = sm;
+    x.sv = sv;
+  }
+};
+
 template <int W, bool GBF16, bool S8, int CAP>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, S8 ? 3 : 4)
 adamw_kernel(const __grid_constant__ Batch<CAP> b, const __grid_constant__ Consts c,
              const float* lr_p, const float* grad_scale, int32_t* step, bool last_launch) {
+  __shared__ __align__(16) char smem[S8 ? Ahead<W, GBF16>::kBytes : 16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tiles = b.first_tile[b.count];
+  int tile = blockIdx.x;
+  int item = 0;  // of this tile: the last tensor that begins at or before it
+  for (int hi = b.count - 1; item < hi;) {
+    const int mid = (item + hi + 1) >> 1;
+    if (b.first_tile[mid] <= tile) item = mid;
+    else hi = mid - 1;
+  }
+  Ahead<W, GBF16> ahead(smem);
+  if constexpr (S8) {
+    const Tile<W, GBF16, S8> tl(b, item, tile);
+    if (tl.n == kTile) ahead.fill(tl, warp, lane);
+    commit_copies();
+  }
   Step st;
   st.scaled = grad_scale != nullptr;
   st.gs = st.scaled ? *grad_scale : 1.f;
-  if (!isfinite(st.gs)) return;  // the same for every CTA: the step is left out as a whole
   const int t = step[0] + 1;
   st.lr = *lr_p;
   st.lr1 = st.lr / -expm1f((float)t * c.log_b1);
   st.inv2 = rsqrtf(-expm1f((float)t * c.log_b2));
-  const int tiles = b.first_tile[b.count];
+  if (!isfinite(st.gs)) {  // the same for every CTA: the step is left out as a whole
+    if constexpr (S8) wait_copies<0>();
+    return;
+  }
 
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    int lo = 0, hi = b.count - 1;  // the last tensor whose first tile is at or before this
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (b.first_tile[mid] <= tile) lo = mid;
-      else hi = mid - 1;
+  while (tile < tiles) {
+    // tiles only rise, so the next one's tensor is this one's or one behind it
+    const int next = tile + (int)gridDim.x;
+    int next_item = next < tiles ? item : b.count;
+    while (next_item < b.count && b.first_tile[next_item + 1] <= next) ++next_item;
+    const Tile<W, GBF16, S8> tl(b, item, tile);
+    Values x;
+    if constexpr (S8) {
+      wait_copies<0>();
+      if (tl.n == kTile) ahead.take(x);
+      const Tile<W, GBF16, S8> nx(b, next_item, next);
+      if (nx.n == kTile) ahead.fill(nx, warp, lane);
+      commit_copies();
     }
-    const Item& it = b.item[lo];
-    const long long block = (long long)(tile - b.first_tile[lo]) * (kThreads / 32) + warp;
-    if ((block + 1) * kBlock <= it.n) update_block<W, GBF16, S8, true>(it, block, lane, c, st);
-    else if (block * kBlock < it.n) update_block<W, GBF16, S8, false>(it, block, lane, c, st);
+    // a tensor's last tile: block by block, each lane looking after its own elements
+    if (tl.n == kTile) {
+      if constexpr (!S8) load_values<W, GBF16, S8, true>(tl, warp, lane, x);
+      step_block<W, GBF16, S8, true>(tl, warp, lane, c, st, x);
+    } else if (warp * kBlock < tl.n) {
+      load_values<W, GBF16, S8, false>(tl, warp, lane, x);
+      step_block<W, GBF16, S8, false>(tl, warp, lane, c, st, x);
+    }
+    tile = next;
+    item = next_item;
   }
   // The last CTA to end raises the step count: all have read it by then.  The ticket wraps
   // to 0 by itself, so nothing has to be cleared between calls.
@@ -354,7 +523,14 @@ cudaError_t launch_batch(const moet_adamw_tensor* const* ts, int count, const Co
   if (err != cudaSuccess) return err;
   const int cap = num_sms() * (per_sm > 0 ? per_sm : 1);
   const int tiles = b.first_tile[count];
-  const int grid = tiles < 1 ? 1 : tiles < cap ? tiles : cap;
+  // fp32 states: up to 16 CTAs one after another in an SM's slot, so that the SMs that memory
+  // serves faster take more of the tiles (50 M weights: 197 us, 222 with one CTA a slot that
+  // stays).  8-bit states: one that stays, since a CTA's start, with no block copied ahead,
+  // costs more than that gives (402 M weights: 857 us, 930 to 1000 with 4 to 32 a slot).
+  const int per_slot = S8 ? 1 : 16;
+  const int most = tiles < cap ? tiles : cap;
+  const int turns = tiles / (cap * per_slot) > 1 ? tiles / (cap * per_slot) : 1;
+  const int grid = tiles < 1 ? 1 : S8 ? most : (tiles + turns - 1) / turns;
   kernel<<<grid, kThreads, 0, st>>>(b, c, lr, gs, step, last);
   return cudaGetLastError();
 }
