@@ -19,6 +19,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kFinalThreads = 512;
+constexpr int kFinalWarps = kFinalThreads / 32;
 constexpr int kChunks = 512;    // chunks a batch is cut into, at most
 constexpr int kMinChunk = 32;   // tokens of a chunk, at least
 
@@ -69,6 +71,22 @@ __device__ __forceinline__ int seq_at(const int32_t* off, int s, int T) {
   return v < 0 ? 0 : v > T ? T : v;
 }
 
+// The last sequence that begins at or before token t (0 when none does), by a warp that
+// probes 32 bounds at a time: one latency for up to 32 sequences, two for up to 1024.
+__device__ __forceinline__ int last_at_or_before(const int32_t* off, int n_seq, int t,
+                                                 int lane) {
+  int lo = 0, n = n_seq;  // the answer is one of the n sequences from lo on
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = lane * step;
+    const unsigned below = __ballot_sync(0xffffffffu, i < n && off[lo + i] <= t);
+    const int k = below ? 31 - __clz(below) : 0;
+    n = min(step, n - k * step);
+    lo += k * step;
+  }
+  return lo;
+}
+
 template <int EPL, int TPW>
 __global__ void __launch_bounds__(kThreads)
 balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids,
@@ -81,6 +99,7 @@ balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restri
   __shared__ int s_n[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int begin = blockIdx.x * chunk, end = min(T, begin + chunk);
+  let_successor_start();  // it waits for this kernel's end; its launch need not
   if (blockIdx.x == 0 && threadIdx.x == 0) *w.ticket = 0;
   for (int e = threadIdx.x; e < 32 * EPL; e += kThreads) s_count[e] = 0;
   bool bad_value = false, bad_id = false;
@@ -90,12 +109,7 @@ balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restri
       if (off[s] < 0 || off[s] > T || (s > 0 && off[s] < off[s - 1]))
         set_status(status, MOET_STATUS_BAD_SEQ);
   }
-  int lo = 0, hi = n_seq - 1;  // the last sequence that begins at or before this chunk
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (seq_at(off, mid, T) <= begin) lo = mid;
-    else hi = mid - 1;
-  }
+  const int lo = off ? last_at_or_before(off, n_seq, begin, lane) : 0;
   int done = begin;  // tokens before it have their lse
   for (int s = lo; s < n_seq; ++s) {
     const int from = max(done, seq_at(off, s, T));
@@ -112,18 +126,28 @@ balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restri
     int n = 0;
     __syncthreads();  // the counts are cleared, the last sequence's sums are read
     for (int t0 = from + warp * TPW; t0 < to; t0 += kWarps * TPW) {
+      // the rows, their masks and their choices at once: a masked row is read and not used
       float x[TPW][EPL], top[TPW], sum[TPW];
       bool on[TPW];
+      int id[TPW];
 #pragma unroll
       for (int u = 0; u < TPW; ++u) {
-        on[u] = t0 + u < to && (!mask || mask[t0 + u]);
-        top[u] = -INFINITY;
+        const bool row = t0 + u < to;
+        on[u] = row && (!mask || mask[t0 + u]);
+        id[u] = row && lane < k ? __ldg(ids + (long long)(t0 + u) * k + lane) : 0;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
           const int e = lane + 32 * i;
-          const bool in = on[u] && e < E;
-          x[u][i] = in ? __ldg(logits + (long long)(t0 + u) * E + e) : -INFINITY;
-          bad_value |= in && !isfinite(x[u][i]);
+          x[u][i] = row && e < E ? __ldg(logits + (long long)(t0 + u) * E + e) : -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < TPW; ++u) {
+        top[u] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          if (!on[u]) x[u][i] = -INFINITY;
+          bad_value |= on[u] && lane + 32 * i < E && !isfinite(x[u][i]);
           top[u] = fmaxf(top[u], x[u][i]);
         }
       }
@@ -158,8 +182,7 @@ balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restri
         z = fmaf(lse, lse, z);
         ++n;
         if (lane < k) {
-          const int e = ids[(long long)(t0 + u) * k + lane];
-          if (e >= 0 && e < E) atomicAdd(&s_count[e], 1);
+          if (id[u] >= 0 && id[u] < E) atomicAdd(&s_count[id[u]], 1);
           else bad_id = true;
         }
       }
@@ -197,15 +220,15 @@ balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restri
   if (bad_id) set_status(status, MOE_STATUS_BAD_ID);
 }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kFinalThreads)
 balance_final_kernel(const int32_t* __restrict__ off, int T, int E, int k, int n_seq, int chunk,
                      int n_slices, Workspace w, float* __restrict__ losses,
                      int32_t* __restrict__ counts, float* __restrict__ probs,
                      int32_t* seq_info) {
-  __shared__ float s_p[kWarps][32];
-  __shared__ int32_t s_c[kWarps][32];
-  __shared__ float s_z[kWarps];
-  __shared__ int32_t s_n[kWarps];
+  __shared__ float s_p[kFinalWarps][32];
+  __shared__ int32_t s_c[kFinalWarps][32];
+  __shared__ float s_z[kFinalWarps];
+  __shared__ int32_t s_n[kFinalWarps];
   __shared__ bool s_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   wait_for_predecessor();
@@ -217,14 +240,15 @@ balance_final_kernel(const int32_t* __restrict__ off, int T, int E, int k, int n
     int32_t c = 0, n = 0;
     if (to > from) {
       const int i0 = from / chunk, i1 = (to - 1) / chunk;
-      for (int i = i0 + warp; i <= i1; i += kWarps) {
-        const long long row = (long long)i + s;
-        if (e < E) {
+      if (e < E) {
+#pragma unroll 8
+        for (int i = i0 + warp; i <= i1; i += kFinalWarps) {
+          const long long row = (long long)i + s;
           p += w.psum[row * E + e];
           c += w.count[row * E + e];
         }
       }
-      for (int i = i0 + threadIdx.x; i <= i1; i += kThreads) {
+      for (int i = i0 + threadIdx.x; i <= i1; i += kFinalThreads) {
         n += w.tokens[(long long)i + s];
         z += w.zsum[(long long)i + s];
       }
@@ -244,7 +268,7 @@ balance_final_kernel(const int32_t* __restrict__ off, int T, int E, int k, int n
       n = 0;
       z = 0.f;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
+      for (int i = 0; i < kFinalWarps; ++i) {
         n += s_n[i];
         z += s_z[i];
         if (i > 0) {
@@ -276,13 +300,13 @@ balance_final_kernel(const int32_t* __restrict__ off, int T, int E, int k, int n
   }
   __syncthreads();
   if (!s_last) return;
-  __shared__ double d_b[kWarps], d_z[kWarps];
-  __shared__ int32_t i_n[kWarps], i_s[kWarps];
+  __shared__ double d_b[kFinalWarps], d_z[kFinalWarps];
+  __shared__ int32_t i_n[kFinalWarps], i_s[kFinalWarps];
   double b = 0., z = 0.;
   int32_t n = 0, some = 0;
-  for (long long i = threadIdx.x; i < (long long)n_seq * n_slices; i += kThreads)
+  for (long long i = threadIdx.x; i < (long long)n_seq * n_slices; i += kFinalThreads)
     b += (double)__ldcg(w.part + i);
-  for (int s = threadIdx.x; s < n_seq; s += kThreads) {
+  for (int s = threadIdx.x; s < n_seq; s += kFinalThreads) {
     const int32_t ns = __ldcg(seq_info + s);
     z += (double)__ldcg(w.seq_z + s);
     n += ns;
@@ -303,7 +327,7 @@ balance_final_kernel(const int32_t* __restrict__ off, int T, int E, int k, int n
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < kWarps; ++i) {
+    for (int i = 1; i < kFinalWarps; ++i) {
       b += d_b[i];
       z += d_z[i];
       n += i_n[i];
@@ -320,7 +344,7 @@ template <int EPL>
 void launch_partial(const moe_cfg& c, const float* logits, const int32_t* ids,
                     const uint8_t* mask, const int32_t* off, int n_seq, const Workspace& w,
                     float* lse, int32_t* status, cudaStream_t st) {
-  constexpr int TPW = EPL <= 2 ? 4 : 2;
+  constexpr int TPW = EPL <= 4 ? 4 : 2;
   balance_partial_kernel<EPL, TPW><<<num_chunks(c.T), kThreads, 0, st>>>(
       logits, ids, mask, off, c.T, c.E, c.k, n_seq, chunk_tokens(c.T), w, lse, status);
 }
@@ -359,7 +383,7 @@ cudaError_t launch_balance_loss(const moe_cfg& c, const float* logits, const int
   const long long units = (long long)n_seq * n_slices;
   const long long cap = (long long)num_sms() * 8;
   return launch_after(balance_final_kernel, dim3((unsigned)(units < cap ? units : cap)),
-                      dim3(kThreads), 0, st, seq_off, c.T, c.E, c.k, n_seq,
+                      dim3(kFinalThreads), 0, st, seq_off, c.T, c.E, c.k, n_seq,
                       chunk_tokens(c.T), n_slices, w, losses, counts, probs, seq_info);
 }
 

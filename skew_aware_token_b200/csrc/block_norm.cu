@@ -22,27 +22,12 @@ namespace {
 // holds, four per SM of a 148-SM GPU.
 constexpr int kMaxPartials = 592;
 
+constexpr int kFwdThreads = 512;  // of a CTA with several row groups
+
 struct NormArgs {
   int T, d8, W;  // rows, 8-column steps of a row, warps of a row's group
   float inv_d, eps, w_offset, res_scale, out_scale;
 };
-
-// Sum over the group of each of N values, on every thread.  `red` is one of the group's two
-// buffers of N * 32 floats; a caller alternates them, so one barrier a reduction is enough.
-template <int N>
-__device__ __forceinline__ void group_sum(float (&v)[N], int W, int group, int warp, int lane,
-                                          float* red) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-  if (W == 1) return;
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) red[i * 32 + warp] = v[i];
-  }
-  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(W * 32) : "memory");
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < W ? red[i * 32 + lane] : 0.f);
-}
 
 template <class WT>
 __device__ __forceinline__ void load_weight(const WT* w, int v, bool in, float offset,
@@ -54,78 +39,6 @@ __device__ __forceinline__ void load_weight(const WT* w, int v, bool in, float o
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) out[j] = 1.f;
-  }
-}
-
-template <class HT, class WT, int V>
-__global__ void __launch_bounds__(1024)
-block_norm_kernel(const NormArgs a, const HT* h, const float* __restrict__ y,
-                  const float* __restrict__ gate, const WT* __restrict__ w_post,
-                  const WT* __restrict__ w_next, HT* h_out, __nv_bfloat16* __restrict__ x) {
-  extern __shared__ __align__(16) char smem[];
-  const int lane = threadIdx.x & 31;
-  const int group = (threadIdx.x >> 5) / a.W, warp = (threadIdx.x >> 5) % a.W;
-  const int groups = (blockDim.x >> 5) / a.W;
-  float* red = reinterpret_cast<float*>(smem) + group * 64;
-  float wp[V][8], wn[V][8];
-  bool in[V];
-#pragma unroll
-  for (int u = 0; u < V; ++u) {
-    const int v = (u * a.W + warp) * 32 + lane;
-    in[u] = v < a.d8;
-    load_weight(w_post, v, in[u], a.w_offset, wp[u]);
-    load_weight(w_next, v, in[u], a.w_offset, wn[u]);
-  }
-  for (int t = blockIdx.x * groups + group; t < a.T; t += gridDim.x * groups) {
-    float hv[V][8], yv[V][8];
-#pragma unroll
-    for (int u = 0; u < V; ++u) {
-      const long long at = ((long long)t * a.d8 + (u * a.W + warp) * 32 + lane) * 8;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) hv[u][j] = yv[u][j] = 0.f;
-      if (in[u]) {
-        load8(h + at, hv[u]);
-        if (y) load8(y + at, yv[u]);
-      }
-    }
-    if (y) {
-      float scale = a.out_scale;
-      if (gate) scale *= gate[t];
-      if (w_post) {
-        float s[1] = {0.f};
-#pragma unroll
-        for (int u = 0; u < V; ++u)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) s[0] = fmaf(yv[u][j], yv[u][j], s[0]);
-        group_sum(s, a.W, group, warp, lane, red);
-        scale *= rsqrtf(fmaf(s[0], a.inv_d, a.eps));
-      }
-#pragma unroll
-      for (int u = 0; u < V; ++u) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          hv[u][j] = fmaf(yv[u][j] * wp[u][j], scale, hv[u][j] * a.res_scale);
-        if (in[u])
-          store8(h_out + ((long long)t * a.d8 + (u * a.W + warp) * 32 + lane) * 8, hv[u]);
-      }
-    }
-    if (w_next) {
-      float s[1] = {0.f};
-#pragma unroll
-      for (int u = 0; u < V; ++u)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (in[u]) s[0] = fmaf(hv[u][j], hv[u][j], s[0]);
-      group_sum(s, a.W, group, warp, lane, red + 32);
-      const float r = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
-#pragma unroll
-      for (int u = 0; u < V; ++u) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) hv[u][j] *= r * wn[u][j];
-        if (in[u])
-          store8(x + ((long long)t * a.d8 + (u * a.W + warp) * 32 + lane) * 8, hv[u]);
-      }
-    }
   }
 }
 
@@ -152,6 +65,93 @@ struct Slots {
     }
   }
 };
+
+// The sum over the group of one value, on every thread.  `red` is one of the group's buffers of
+// 32 floats; a caller uses two in turn, so one barrier a sum is enough.
+__device__ __forceinline__ float group_sum(float v, int W, int group, int warp, int lane,
+                                           float* red) {
+  v = warp_sum(v);
+  if (W == 1) return v;
+  if (lane == 0) red[warp] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(W * 32) : "memory");
+  return warp_sum(lane < W ? red[lane] : 0.f);
+}
+
+// A thread owns 8 columns of every row of its group, and their weights.  The next row's
+// columns are copied to the thread's slots as soon as this row's are in registers (no thread
+// reads another's slots), so that memory works through both means of a row.
+template <class HT, class WT>
+__global__ void __launch_bounds__(1024)
+block_norm_kernel(const NormArgs a, const HT* h, const float* __restrict__ y,
+                  const float* __restrict__ gate, const WT* __restrict__ w_post,
+                  const WT* __restrict__ w_next, HT* h_out, __nv_bfloat16* __restrict__ x) {
+  constexpr int HU = Slots<HT>::kUnits;
+  extern __shared__ __align__(16) char smem[];
+  const int lane = threadIdx.x & 31;
+  const int group = (threadIdx.x >> 5) / a.W, warp = (threadIdx.x >> 5) % a.W;
+  const int groups = (blockDim.x >> 5) / a.W;
+  const uint32_t pitch = blockDim.x * 16;
+  const uint32_t slot_h = smem_addr(smem) + threadIdx.x * 16, slot_y = slot_h + HU * pitch;
+  float* red = reinterpret_cast<float*>(smem + (HU + 2) * pitch) + group * 64;
+  const int v = warp * 32 + lane;
+  const bool in = v < a.d8;
+  auto ahead = [&](int t) {
+    if (t < a.T && in) {
+      const long long at = ((long long)t * a.d8 + v) * 8;
+      Slots<HT>::fill(slot_h, pitch, h + at);
+      if (y) Slots<float>::fill(slot_y, pitch, y + at);
+    }
+    commit_copies();
+  };
+  const int step = gridDim.x * groups;
+  int t = blockIdx.x * groups + group;
+  ahead(t);
+  float wp[8], wn[8];
+  load_weight(w_post, v, in, a.w_offset, wp);
+  load_weight(w_next, v, in, a.w_offset, wn);
+  for (; t < a.T; t += step) {
+    const long long at = ((long long)t * a.d8 + v) * 8;
+    float scale = a.out_scale;
+    if (gate) scale *= gate[t];
+    float hv[8], yv[8];
+    wait_copies<0>();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) hv[j] = yv[j] = 0.f;
+    if (in) {
+      Slots<HT>::read(slot_h, pitch, hv);
+      if (y) Slots<float>::read(slot_y, pitch, yv);
+    }
+    ahead(t + step);
+    if (y) {
+      if (w_post) {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = fmaf(yv[j], yv[j], s);
+        s = group_sum(s, a.W, group, warp, lane, red);
+        scale *= rsqrtf(fmaf(s, a.inv_d, a.eps));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) hv[j] = fmaf(yv[j] * wp[j], scale, hv[j] * a.res_scale);
+      if (in) store8(h_out + at, hv);
+    }
+    if (w_next) {
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s = fmaf(hv[j], hv[j], s);
+      s = group_sum(s, a.W, group, warp, lane, red + 32);
+      const float r = rsqrtf(fmaf(s, a.inv_d, a.eps));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) hv[j] *= r * wn[j];
+      if (in) store8(x + at, hv);
+    }
+  }
+}
+
+__device__ __forceinline__ void read4(uint32_t slot, float* v) {
+  const uint4 a = slot16(slot);
+  v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y);
+  v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
+}
 
 // The six sums of a row over its group of W warps, on every thread.  `red`: 8 * 17 floats.
 __device__ __forceinline__ void group_sum8(float (&v)[8], int W, int group, int warp, int lane,
@@ -205,6 +205,7 @@ block_norm_backward_kernel(const NormArgs a, const HT* __restrict__ h_out,
                 kWn = kWp + 2 * V;
   bool in[V];
   float gp[V][8], gn[V][8];
+  let_successor_start();  // it waits for this kernel's end; its launch need not
 #pragma unroll
   for (int u = 0; u < V; ++u) {
     const int v = (u * a.W + warp) * 32 + lane;
@@ -253,13 +254,14 @@ block_norm_backward_kernel(const NormArgs a, const HT* __restrict__ h_out,
     ahead(t + step);
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int u = 0; u < V; ++u) {
-      float wp[8], wn[8];
-      Slots<float>::read(slot(kWp + 2 * u), pitch, wp);
-      Slots<float>::read(slot(kWn + 2 * u), pitch, wn);
+    for (int i = 0; i < 2 * V; ++i) {
+      float wp[4], wn[4];
+      read4(slot(kWp + i), wp);
+      read4(slot(kWn + i), wn);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float qw = q[u][j] * wn[j], yw = yv[u][j] * wp[j];
+      for (int k = 0; k < 4; ++k) {
+        const int u = i / 2, j = 4 * (i % 2) + k;
+        const float qw = q[u][j] * wn[k], yw = yv[u][j] * wp[k];
         s[0] = fmaf(hv[u][j], hv[u][j], s[0]);
         s[1] = fmaf(qw, hv[u][j], s[1]);
         s[2] = fmaf(yv[u][j], yv[u][j], s[2]);
@@ -281,20 +283,22 @@ block_norm_backward_kernel(const NormArgs a, const HT* __restrict__ h_out,
     const float res = y ? a.res_scale : 1.f;
     if (gate && warp == 0 && lane == 0) dgate[t] = a.out_scale * ry * uy;
 #pragma unroll
-    for (int u = 0; u < V; ++u) {
-      float wp[8], wn[8];
-      Slots<float>::read(slot(kWp + 2 * u), pitch, wp);
-      Slots<float>::read(slot(kWn + 2 * u), pitch, wn);
-      const long long at = ((long long)t * a.d8 + (u * a.W + warp) * 32 + lane) * 8;
+    for (int i = 0; i < 2 * V; ++i) {
+      const int u = i / 2;
+      float wp[4], wn[4];
+      read4(slot(kWp + i), wp);
+      read4(slot(kWn + i), wn);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int k = 0; k < 4; ++k) {
+        const int j = 4 * (i % 2) + k;
         gn[u][j] = fmaf(q[u][j] * A, hv[u][j], gn[u][j]);
-        const float g = fmaf(q[u][j] * wn[j], A, fmaf(-B, hv[u][j], u8[u][j]));
+        const float g = fmaf(q[u][j] * wn[k], A, fmaf(-B, hv[u][j], u8[u][j]));
         gp[u][j] = fmaf(g * scale, yv[u][j], gp[u][j]);
-        yv[u][j] = scale * fmaf(g, wp[j], -yv[u][j] * back);
+        yv[u][j] = scale * fmaf(g, wp[k], -yv[u][j] * back);
         u8[u][j] = g * res;
       }
-      if (in[u]) {
+      if (i % 2 == 1 && in[u]) {
+        const long long at = ((long long)t * a.d8 + (u * a.W + warp) * 32 + lane) * 8;
         if (y) store8(dy + at, yv[u]);
         store8(dh + at, u8[u]);
       }
@@ -327,21 +331,26 @@ block_norm_backward_kernel(const NormArgs a, const HT* __restrict__ h_out,
   }
 }
 
-// dw = sum of `rows` partial rows, 32 columns a CTA, 8 rows at a time.
-__global__ void __launch_bounds__(256)
+// dw = sum of `rows` partial rows: 32 columns a CTA, its warps take the rows in turn and are
+// added in order.
+constexpr int kSumWarps = 16;
+__global__ void __launch_bounds__(kSumWarps * 32)
 norm_weight_grad_kernel(const float* __restrict__ partial, int rows, int d,
                         float* __restrict__ dw_post, float* __restrict__ dw_next) {
-  __shared__ float part[8][32];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), lane_row = threadIdx.x >> 5;
+  __shared__ float part[kSumWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
   wait_for_predecessor();
   float s = 0.f;
-  if (col < 2 * d)
-    for (int r = lane_row; r < rows; r += 8) s += partial[(long long)r * 2 * d + col];
-  part[lane_row][threadIdx.x & 31] = s;
+  if (col < 2 * d) {
+#pragma unroll 8
+    for (int r = warp; r < rows; r += kSumWarps) s += partial[(long long)r * 2 * d + col];
+  }
+  part[warp][lane] = s;
   __syncthreads();
-  if (lane_row == 0 && col < 2 * d) {
+  if (warp == 0 && col < 2 * d) {
 #pragma unroll
-    for (int r = 1; r < 8; ++r) s += part[r][threadIdx.x & 31];
+    for (int r = 1; r < kSumWarps; ++r) s += part[r][lane];
     if (col < d) {
       if (dw_post) dw_post[col] = s;
     } else if (dw_next) {
@@ -362,17 +371,30 @@ NormArgs make_args(const moe_cfg& c, const moet_norm& n, int V) {
   a.out_scale = n.out_scale;
   return a;
 }
-// row groups of a CTA: about 256 threads
-int groups_of(int W) { return W >= 8 ? 1 : 8 / W; }
+// Row groups of a CTA: as many as `threads` hold, but no more than it takes to give every SM
+// rows.
+int groups_of(int T, int W, int threads) {
+  const int fit = threads / 32 / W, sms = num_sms(), rows = (T + sms - 1) / sms;
+  const int n = fit < rows ? fit : rows;
+  return n < 1 ? 1 : n;
+}
 
-template <class HT, class WT, int V>
+template <class HT, class WT>
 cudaError_t forward(const moe_cfg& c, const moet_norm& n, const void* h, const float* y,
                     const float* gate, const void* wp, const void* wn, void* h_out,
                     uint16_t* x, cudaStream_t st) {
-  const NormArgs a = make_args(c, n, V);
-  const int groups = groups_of(a.W), threads = groups * a.W * 32;
-  const int want = (c.T + groups - 1) / groups, cap = num_sms() * (2048 / threads);
-  block_norm_kernel<HT, WT, V><<<want < cap ? want : cap, threads, groups * 64 * 4, st>>>(
+  constexpr int kUnits = Slots<HT>::kUnits + 2;
+  const NormArgs a = make_args(c, n, 1);
+  const int groups = groups_of(c.T, a.W, kFwdThreads), threads = groups * a.W * 32;
+  auto kernel = block_norm_kernel<HT, WT>;
+  static OncePerDevice once;
+  const cudaError_t err = once_per_device(once, [&](int&) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kUnits * 1024 * 16 + 16 * 64 * 4);
+  });
+  if (err != cudaSuccess) return err;
+  const int want = (c.T + groups - 1) / groups, cap = num_sms() * (1024 / threads);
+  kernel<<<want < cap ? want : cap, threads, kUnits * threads * 16 + groups * 64 * 4, st>>>(
       a, static_cast<const HT*>(h), y, gate, static_cast<const WT*>(wp),
       static_cast<const WT*>(wn), static_cast<HT*>(h_out),
       reinterpret_cast<__nv_bfloat16*>(x));
@@ -386,18 +408,13 @@ cudaError_t backward(const moe_cfg& c, const moet_norm& n, const void* h_out, co
                      float* dw_next, void* ws, cudaStream_t st) {
   const NormArgs a = make_args(c, n, kBwdV);
   const int sms = num_sms();
-  // as many row groups as fit the CTA, but no more than it takes to give every SM rows
-  int groups = kBwdThreads / 32 / a.W;
-  const int rows_per_sm = (c.T + sms - 1) / sms;
-  if (groups > rows_per_sm) groups = rows_per_sm;
-  if (groups < 1) groups = 1;
-  const int threads = groups * a.W * 32;
+  const int groups = groups_of(c.T, a.W, kBwdThreads), threads = groups * a.W * 32;
   const size_t smem = (size_t)bwd_units<HT>() * threads * 16 + (size_t)groups * kBwdRed * 4;
   auto kernel = block_norm_backward_kernel<HT, WT>;
   static OncePerDevice once;
   cudaError_t err = once_per_device(once, [&](int&) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                bwd_units<HT>() * kBwdThreads * 16 + 16 * kBwdRed * 4);
+                                bwd_units<HT>() * kBwdThreads * 16 + kBwdThreads / 32 * kBwdRed * 4);
   });
   if (err != cudaSuccess) return err;
   int grid = (c.T + groups - 1) / groups;
@@ -413,7 +430,8 @@ cudaError_t backward(const moe_cfg& c, const moet_norm& n, const void* h_out, co
     if (err != cudaSuccess) return err;
   }
   if (!dw_post && !dw_next) return cudaSuccess;
-  return launch_after(norm_weight_grad_kernel, dim3((2 * c.d + 31) / 32), dim3(256), 0, st,
+  return launch_after(norm_weight_grad_kernel, dim3((2 * c.d + 31) / 32),
+                      dim3(kSumWarps * 32), 0, st,
                       static_cast<const float*>(ws), grid, c.d, dw_post, dw_next);
 }
 
@@ -431,9 +449,7 @@ cudaError_t launch_block_norm(const moe_cfg& c, const moet_norm& n, const void* 
   auto run = [&](auto ht, auto wt) {
     using HT = decltype(ht);
     using WT = decltype(wt);
-    if (c.T < num_sms())
-      return forward<HT, WT, 1>(c, n, h, y, gate, w_post, w_next, h_out, x, st);
-    return forward<HT, WT, 2>(c, n, h, y, gate, w_post, w_next, h_out, x, st);
+    return forward<HT, WT>(c, n, h, y, gate, w_post, w_next, h_out, x, st);
   };
   const bool hb = n.h_dtype == MOET_BF16, wb = n.w_dtype == MOET_BF16;
   if (hb) return wb ? run(__nv_bfloat16(), __nv_bfloat16()) : run(__nv_bfloat16(), 0.f);

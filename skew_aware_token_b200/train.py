@@ -21,6 +21,7 @@ its outputs are views that the next call overwrites.
 """
 from __future__ import annotations
 
+import array
 import collections
 import ctypes
 import operator
@@ -51,6 +52,10 @@ def _need(t, name, dtype, n, dev, optional=False):
         if optional:
             return None
         raise TypeError(f"{name} is needed")
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n and \
+            t.get_device() == dev.index and t.is_contiguous():
+        return t.data_ptr()
+    # what is wrong with it, or a flat buffer
     if not isinstance(t, torch.Tensor) or t.get_device() != dev.index:
         raise TypeError(f"{name} must be a tensor on {dev}")
     if t.dtype is not dtype:
@@ -61,13 +66,23 @@ def _need(t, name, dtype, n, dev, optional=False):
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (a fifth of a small call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_stream(dev) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
 class _OnDevice:
     """Runs a call with the object's device current and the stream resolved on it."""
 
     def _call(self, fn, *args, stream=None):
         dev = self.device
         if stream is None:
-            stream = torch.cuda.current_stream(dev).cuda_stream
+            stream = _current_stream(dev)
         elif isinstance(stream, torch.cuda.Stream) and stream.device != dev:
             raise ValueError(f"the stream is on {stream.device}, the arrays on {dev}")
         if torch.cuda.current_device() == dev.index:
@@ -352,6 +367,7 @@ class AdamW(_OnDevice):
              "itemsize": ctypes.sizeof(N.MoetAdamwTensor)}))
         self._g, self._g_dtype = fields["g"], fields["g_dtype"]
         self._devices = [dev.index] * count
+        self._types = None  # of the last step's gradients, as the descriptors hold them
         self._opt = N.MoetAdamw(float(betas[0]), float(betas[1]), float(eps))
         self.lr = torch.full((4,), float(lr), device=dev)
         self.steps = torch.tensor([step, 0, 0, 0], dtype=torch.int32, device=dev)
@@ -368,18 +384,22 @@ class AdamW(_OnDevice):
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
         # over all of them at once: a loop over hundreds of tensors costs more than the step
-        if not all(isinstance(g, torch.Tensor) for g in grads):
-            raise TypeError("grads must be tensors")
-        types = list(map(_dtype_of, grads))
-        if not _GRAD_TYPES.issuperset(types):
-            raise TypeError("grads must be torch.float32 or torch.bfloat16 tensors")
-        if list(map(torch.Tensor.get_device, grads)) != self._devices:
+        try:
+            types = list(map(_dtype_of, grads))
+            devices = list(map(torch.Tensor.get_device, grads))
+        except (AttributeError, TypeError):
+            raise TypeError("grads must be tensors") from None
+        if devices != self._devices:
             raise TypeError(f"grads must be on {self.device}")
+        if types != self._types:
+            if not _GRAD_TYPES.issuperset(types):
+                raise TypeError("grads must be torch.float32 or torch.bfloat16 tensors")
+            self._g_dtype[:] = list(map(_TYPES.__getitem__, types))
+            self._types = types
         if list(map(torch.Tensor.numel, grads)) != self._sizes or \
                 not all(map(torch.Tensor.is_contiguous, grads)):
             raise ValueError("grads must be contiguous and of their parameters' sizes")
-        self._g[:] = list(map(torch.Tensor.data_ptr, grads))
-        self._g_dtype[:] = list(map(_TYPES.__getitem__, types))
+        self._g[:] = array.array("Q", map(torch.Tensor.data_ptr, grads))
         scale = _need(grad_scale, "grad_scale", torch.float32, 1, self.device, True)
         self._call(N.moet_adamw_step, self._tensors, len(grads), self._opt, self.lr, scale,
                    self.steps, stream=stream)
