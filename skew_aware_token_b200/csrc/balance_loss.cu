@@ -8,10 +8,11 @@
 // a sequence's end adds the warps' columns in warp order into one partial row.  Chunk i's
 // part of sequence s goes to row i + s: both only rise along the tokens, and one of them
 // rises from each (chunk, sequence) pair that meets to the next, so no two share a row.
-// Second kernel: a CTA per sequence and 32 experts adds that sequence's partial rows in chunk
+// Second kernel (the same one, behind a cluster barrier, for a small batch): a CTA per sequence and 32 experts adds that sequence's partial rows in chunk
 // order; the last CTA to end adds the sequences' losses in order.  No atomics on values: the
-// same bits on every run.  Bound by reading the logits once, for all but the largest layers
-// by the two launches.
+// same bits on every run.  The traffic is the logits once (16384 x 256: 2.6 us of HBM); what
+// bounds it are the two dependent kernels, each a chain of loads, sums and barriers: 12.9 us
+// at that size, 12.8 us on 24 packed sequences of 128 experts.
 #include "train_common.cuh"
 
 namespace moe {
@@ -21,11 +22,15 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kFinalThreads = 512;
 constexpr int kFinalWarps = kFinalThreads / 32;
-constexpr int kChunks = 512;    // chunks a batch is cut into, at most
+constexpr int kChunks = 296;    // chunks a batch is cut into, at most (2 for each of 148 SMs)
 constexpr int kMinChunk = 32;   // tokens of a chunk, at least
 
+constexpr int kCluster = 8;     // CTAs that a small batch takes in one launch
+constexpr int kSmallTokens = 256;
+
 int chunk_tokens(int T) {
-  const int c = (T + kChunks - 1) / kChunks;
+  const int n = T <= kSmallTokens ? kCluster : kChunks;
+  const int c = (T + n - 1) / n;
   return c < kMinChunk ? kMinChunk : c;
 }
 int num_chunks(int T) { return T > 0 ? (T + chunk_tokens(T) - 1) / chunk_tokens(T) : 0; }
@@ -87,20 +92,44 @@ __device__ __forceinline__ int last_at_or_before(const int32_t* off, int n_seq, 
   return lo;
 }
 
+struct Batch {
+  const float* logits;
+  const int32_t* ids;
+  const uint8_t* mask;
+  const int32_t* off;
+  int T, E, k, n_seq, chunk, n_slices;
+};
+struct Results {
+  float* losses;
+  int32_t* counts;
+  float* probs;
+  int32_t* seq_info;
+  float* lse;
+  int32_t* status;
+};
+
+__device__ __forceinline__ float exp2_near(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The partial rows of one chunk (the CTA's).
 template <int EPL, int TPW>
-__global__ void __launch_bounds__(kThreads)
-balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids,
-                       const uint8_t* __restrict__ mask, const int32_t* __restrict__ off,
-                       int T, int E, int k, int n_seq, int chunk, Workspace w,
-                       float* __restrict__ lse_out, int32_t* __restrict__ status) {
+__device__ __forceinline__ void chunk_sums(const Batch& b, const Workspace& w, const Results& r) {
+  const float* __restrict__ logits = b.logits;
+  const int32_t* __restrict__ ids = b.ids;
+  const uint8_t* __restrict__ mask = b.mask;
+  const int32_t* __restrict__ off = b.off;
+  const int T = b.T, E = b.E, k = b.k, n_seq = b.n_seq, chunk = b.chunk;
+  float* lse_out = r.lse;
+  int32_t* status = r.status;
   __shared__ float s_p[kWarps][32 * EPL];
   __shared__ int32_t s_count[32 * EPL];
   __shared__ float s_z[kWarps];
   __shared__ int s_n[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int begin = blockIdx.x * chunk, end = min(T, begin + chunk);
-  let_successor_start();  // it waits for this kernel's end; its launch need not
-  if (blockIdx.x == 0 && threadIdx.x == 0) *w.ticket = 0;
   for (int e = threadIdx.x; e < 32 * EPL; e += kThreads) s_count[e] = 0;
   bool bad_value = false, bad_id = false;
   if (off) {
@@ -122,7 +151,7 @@ balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restri
     float acc[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
-    float z = 0.f;
+    float z = 0.f;  // of the tokens whose lane of a turn this is
     int n = 0;
     __syncthreads();  // the counts are cleared, the last sequence's sums are read
     for (int t0 = from + warp * TPW; t0 < to; t0 += kWarps * TPW) {
@@ -143,26 +172,24 @@ balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restri
       }
 #pragma unroll
       for (int u = 0; u < TPW; ++u) {
-        top[u] = -INFINITY;
+        float zero = 0.f;  // NaN if a logit is not finite
+        top[u] = x[u][0];
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-          if (!on[u]) x[u][i] = -INFINITY;
-          bad_value |= on[u] && lane + 32 * i < E && !isfinite(x[u][i]);
-          top[u] = fmaxf(top[u], x[u][i]);
+          if (lane + 32 * i < E) zero = fmaf(x[u][i], 0.f, zero);
+          if (i > 0) top[u] = fmaxf(top[u], x[u][i]);
         }
+        bad_value |= on[u] && zero != 0.f;
+        asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top[u]) : "f"(top[u]));
       }
-#pragma unroll
-      for (int off2 = 16; off2 > 0; off2 >>= 1)
-#pragma unroll
-        for (int u = 0; u < TPW; ++u)
-          top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], off2));
+      // e^(x - top) = 2^((x - top) log2 e): the argument's rounding, 2^-24 of it, is a relative
+      // error of p that falls as p does, under 2^-22 where p > 1/16
 #pragma unroll
       for (int u = 0; u < TPW; ++u) {
-        if (top[u] == -INFINITY) top[u] = 0.f;  // a row of nothing: exponentials of 0
         sum[u] = 0.f;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-          x[u][i] = expf(x[u][i] - top[u]);
+          x[u][i] = exp2_near((x[u][i] - top[u]) * 1.44269504f);
           sum[u] += x[u][i];
         }
       }
@@ -170,23 +197,31 @@ balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restri
       for (int off2 = 16; off2 > 0; off2 >>= 1)
 #pragma unroll
         for (int u = 0; u < TPW; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], off2);
+      // lane u: token u's lse
+      float my_sum = 1.f, my_top = 0.f;
+      bool my_on = false;
 #pragma unroll
       for (int u = 0; u < TPW; ++u) {
-        if (t0 + u >= to) continue;
-        const float lse = on[u] ? top[u] + logf(sum[u]) : 0.f;
-        if (lane == 0) lse_out[t0 + u] = lse;
+        if (lane == u) {
+          my_sum = sum[u];
+          my_top = top[u];
+          my_on = on[u];
+        }
         if (!on[u]) continue;
-        const float inv = sum[u] > 0.f ? 1.f / sum[u] : 0.f;
+        const float inv = __fdividef(1.f, sum[u]);
 #pragma unroll
         for (int i = 0; i < EPL; ++i) acc[i] = fmaf(x[u][i], inv, acc[i]);
-        z = fmaf(lse, lse, z);
         ++n;
         if (lane < k) {
           if (id[u] >= 0 && id[u] < E) atomicAdd(&s_count[id[u]], 1);
           else bad_id = true;
         }
       }
+      const float lse = my_on ? my_top + logf(my_sum) : 0.f;
+      if (lane < TPW && t0 + lane < to) lse_out[t0 + lane] = lse;
+      z = fmaf(lse, lse, z);
     }
+    z = warp_sum(z);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) s_p[warp][lane + 32 * i] = acc[i];
     if (lane == 0) {
@@ -220,21 +255,25 @@ balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restri
   if (bad_id) set_status(status, MOE_STATUS_BAD_ID);
 }
 
-__global__ void __launch_bounds__(kFinalThreads)
-balance_final_kernel(const int32_t* __restrict__ off, int T, int E, int k, int n_seq, int chunk,
-                     int n_slices, Workspace w, float* __restrict__ losses,
-                     int32_t* __restrict__ counts, float* __restrict__ probs,
-                     int32_t* seq_info) {
-  __shared__ float s_p[kFinalWarps][32];
-  __shared__ int32_t s_c[kFinalWarps][32];
-  __shared__ float s_z[kFinalWarps];
-  __shared__ int32_t s_n[kFinalWarps];
-  __shared__ bool s_last;
+// The units (a sequence's 32 experts) of this CTA: counts, mean probabilities, part of the loss.
+template <int WARPS, bool WAIT>
+__device__ __forceinline__ void sequence_sums(const Batch& b, const Workspace& w,
+                                              const Results& out) {
+  __shared__ float s_p[WARPS][32];
+  __shared__ int32_t s_c[WARPS][32];
+  __shared__ float s_z[WARPS];
+  __shared__ int32_t s_n[WARPS];
+  const int32_t* off = b.off;
+  const int T = b.T, E = b.E, n_seq = b.n_seq, chunk = b.chunk, n_slices = b.n_slices;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  wait_for_predecessor();
+  bool waited = !WAIT;
   for (long long unit = blockIdx.x; unit < (long long)n_seq * n_slices; unit += gridDim.x) {
     const int s = (int)(unit / n_slices), slice = (int)(unit % n_slices);
     const int from = seq_at(off, s, T), to = seq_at(off, s + 1, T);
+    if (!waited) {  // the bounds are the caller's, what follows is the first kernel's
+      wait_for_predecessor();
+      waited = true;
+    }
     const int e = slice * 32 + lane;
     float p = 0.f, z = 0.f;
     int32_t c = 0, n = 0;
@@ -242,13 +281,13 @@ balance_final_kernel(const int32_t* __restrict__ off, int T, int E, int k, int n
       const int i0 = from / chunk, i1 = (to - 1) / chunk;
       if (e < E) {
 #pragma unroll 8
-        for (int i = i0 + warp; i <= i1; i += kFinalWarps) {
+        for (int i = i0 + warp; i <= i1; i += WARPS) {
           const long long row = (long long)i + s;
           p += w.psum[row * E + e];
           c += w.count[row * E + e];
         }
       }
-      for (int i = i0 + threadIdx.x; i <= i1; i += kFinalThreads) {
+      for (int i = i0 + threadIdx.x; i <= i1; i += WARPS * 32) {
         n += w.tokens[(long long)i + s];
         z += w.zsum[(long long)i + s];
       }
@@ -268,7 +307,7 @@ balance_final_kernel(const int32_t* __restrict__ off, int T, int E, int k, int n
       n = 0;
       z = 0.f;
 #pragma unroll
-      for (int i = 0; i < kFinalWarps; ++i) {
+      for (int i = 0; i < WARPS; ++i) {
         n += s_n[i];
         z += s_z[i];
         if (i > 0) {
@@ -278,36 +317,35 @@ balance_final_kernel(const int32_t* __restrict__ off, int T, int E, int k, int n
       }
       const float mean = n > 0 ? p / (float)n : 0.f;
       if (e < E) {
-        probs[(long long)s * E + e] = mean;
-        counts[(long long)s * E + e] = c;
+        out.probs[(long long)s * E + e] = mean;
+        out.counts[(long long)s * E + e] = c;
       }
       const float dot = warp_sum(e < E ? mean * (float)c : 0.f);
       if (lane == 0) {
         w.part[unit] = n > 0 ? dot / (float)n : 0.f;
         if (slice == 0) {
-          seq_info[s] = n;
+          out.seq_info[s] = n;
           w.seq_z[s] = z;
         }
       }
     }
   }
-  // the last CTA to end adds the sequences
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    s_last = atomicAdd(w.ticket, 1u) == gridDim.x - 1;
-    __threadfence();
-  }
-  __syncthreads();
-  if (!s_last) return;
-  __shared__ double d_b[kFinalWarps], d_z[kFinalWarps];
-  __shared__ int32_t i_n[kFinalWarps], i_s[kFinalWarps];
+}
+
+// The losses, from every sequence's parts in order (one CTA).
+template <int WARPS>
+__device__ __forceinline__ void batch_sums(const Batch& bt, const Workspace& w,
+                                           const Results& out) {
+  const int E = bt.E, k = bt.k, n_seq = bt.n_seq, n_slices = bt.n_slices;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ double d_b[WARPS], d_z[WARPS];
+  __shared__ int32_t i_n[WARPS], i_s[WARPS];
   double b = 0., z = 0.;
   int32_t n = 0, some = 0;
-  for (long long i = threadIdx.x; i < (long long)n_seq * n_slices; i += kFinalThreads)
+  for (long long i = threadIdx.x; i < (long long)n_seq * n_slices; i += WARPS * 32)
     b += (double)__ldcg(w.part + i);
-  for (int s = threadIdx.x; s < n_seq; s += kFinalThreads) {
-    const int32_t ns = __ldcg(seq_info + s);
+  for (int s = threadIdx.x; s < n_seq; s += WARPS * 32) {
+    const int32_t ns = __ldcg(out.seq_info + s);
     z += (double)__ldcg(w.seq_z + s);
     n += ns;
     some += ns > 0;
@@ -327,26 +365,77 @@ balance_final_kernel(const int32_t* __restrict__ off, int T, int E, int k, int n
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < kFinalWarps; ++i) {
+    for (int i = 1; i < WARPS; ++i) {
       b += d_b[i];
       z += d_z[i];
       n += i_n[i];
       some += i_s[i];
     }
-    losses[0] = some > 0 ? (float)(b * E / ((double)k * some)) : 0.f;
-    losses[1] = n > 0 ? (float)(z / n) : 0.f;
-    seq_info[n_seq] = n;
-    seq_info[n_seq + 1] = some;
+    out.losses[0] = some > 0 ? (float)(b * E / ((double)k * some)) : 0.f;
+    out.losses[1] = n > 0 ? (float)(z / n) : 0.f;
+    out.seq_info[n_seq] = n;
+    out.seq_info[n_seq + 1] = some;
   }
 }
 
+template <int EPL, int TPW>
+__global__ void __launch_bounds__(kThreads, 4)
+balance_partial_kernel(const Batch b, const Workspace w, const Results r) {
+  let_successor_start();  // it waits for this kernel's end; its launch need not
+  if (blockIdx.x == 0 && threadIdx.x == 0) *w.ticket = 0;
+  chunk_sums<EPL, TPW>(b, w, r);
+}
+
+__global__ void __launch_bounds__(kFinalThreads)
+balance_final_kernel(const Batch b, const Workspace w, const Results r) {
+  __shared__ bool s_last;
+  sequence_sums<kFinalWarps, true>(b, w, r);
+  // the last CTA to end adds the sequences
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(w.ticket, 1u) == gridDim.x - 1;
+    __threadfence();
+  }
+  __syncthreads();
+  if (s_last) batch_sums<kFinalWarps>(b, w, r);
+}
+
+// Both in one launch of one cluster: its barrier, which orders the CTAs' writes, stands
+// between the steps.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+template <int EPL, int TPW>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+balance_small_kernel(const Batch b, const Workspace w, const Results r) {
+  chunk_sums<EPL, TPW>(b, w, r);
+  __syncthreads();
+  cluster_barrier();
+  sequence_sums<kWarps, false>(b, w, r);
+  __syncthreads();
+  cluster_barrier();
+  if (blockIdx.x == 0) batch_sums<kWarps>(b, w, r);
+}
+
 template <int EPL>
-void launch_partial(const moe_cfg& c, const float* logits, const int32_t* ids,
-                    const uint8_t* mask, const int32_t* off, int n_seq, const Workspace& w,
-                    float* lse, int32_t* status, cudaStream_t st) {
-  constexpr int TPW = EPL <= 4 ? 4 : 2;
-  balance_partial_kernel<EPL, TPW><<<num_chunks(c.T), kThreads, 0, st>>>(
-      logits, ids, mask, off, c.T, c.E, c.k, n_seq, chunk_tokens(c.T), w, lse, status);
+cudaError_t launch(const Batch& b, const Workspace& w, const Results& r, cudaStream_t st) {
+  constexpr int TPW = EPL <= 2 ? 4 : 2;
+  const long long units = (long long)b.n_seq * b.n_slices;
+  // A small batch of few sequences takes one launch: 256 tokens of 8 experts 6.7 us against
+  // 8.2 us in two launches; from 512 tokens on (8.3 against 8.0 us) the chunks of 8 CTAs are
+  // too long.
+  if (b.T <= kSmallTokens && units <= kCluster * 4) {
+    balance_small_kernel<EPL, TPW><<<kCluster, kThreads, 0, st>>>(b, w, r);
+    return cudaGetLastError();
+  }
+  balance_partial_kernel<EPL, TPW><<<b.T ? num_chunks(b.T) : 1, kThreads, 0, st>>>(b, w, r);
+  const cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  const long long cap = (long long)num_sms() * 8;
+  return launch_after(balance_final_kernel, dim3((unsigned)(units < cap ? units : cap)),
+                      dim3(kFinalThreads), 0, st, b, w, r);
 }
 
 }  // namespace
@@ -362,29 +451,19 @@ cudaError_t launch_balance_loss(const moe_cfg& c, const float* logits, const int
                                 cudaStream_t st) {
   Workspace w;
   layout(c, n_seq, ws, &w);
-  if (c.T == 0) {
-    const cudaError_t err = cudaMemsetAsync(w.ticket, 0, 4, st);
-    if (err != cudaSuccess) return err;
-  } else {
-    switch ((c.E + 31) / 32) {
-      case 1: launch_partial<1>(c, logits, ids, mask, seq_off, n_seq, w, lse, status, st); break;
-      case 2: launch_partial<2>(c, logits, ids, mask, seq_off, n_seq, w, lse, status, st); break;
-      case 3: launch_partial<3>(c, logits, ids, mask, seq_off, n_seq, w, lse, status, st); break;
-      case 4: launch_partial<4>(c, logits, ids, mask, seq_off, n_seq, w, lse, status, st); break;
-      case 5: launch_partial<5>(c, logits, ids, mask, seq_off, n_seq, w, lse, status, st); break;
-      case 6: launch_partial<6>(c, logits, ids, mask, seq_off, n_seq, w, lse, status, st); break;
-      case 7: launch_partial<7>(c, logits, ids, mask, seq_off, n_seq, w, lse, status, st); break;
-      default: launch_partial<8>(c, logits, ids, mask, seq_off, n_seq, w, lse, status, st); break;
-    }
-    const cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
+  const Batch b = {logits, ids,   mask,  seq_off,           c.T,
+                   c.E,    c.k,   n_seq, chunk_tokens(c.T), slices(c.E)};
+  const Results r = {losses, counts, probs, seq_info, lse, status};
+  switch ((c.E + 31) / 32) {
+    case 1: return launch<1>(b, w, r, st);
+    case 2: return launch<2>(b, w, r, st);
+    case 3: return launch<3>(b, w, r, st);
+    case 4: return launch<4>(b, w, r, st);
+    case 5: return launch<5>(b, w, r, st);
+    case 6: return launch<6>(b, w, r, st);
+    case 7: return launch<7>(b, w, r, st);
+    default: return launch<8>(b, w, r, st);
   }
-  const int n_slices = slices(c.E);
-  const long long units = (long long)n_seq * n_slices;
-  const long long cap = (long long)num_sms() * 8;
-  return launch_after(balance_final_kernel, dim3((unsigned)(units < cap ? units : cap)),
-                      dim3(kFinalThreads), 0, st, seq_off, c.T, c.E, c.k, n_seq,
-                      chunk_tokens(c.T), n_slices, w, losses, counts, probs, seq_info);
 }
 
 }  // namespace moe

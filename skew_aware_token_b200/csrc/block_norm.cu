@@ -206,20 +206,12 @@ block_norm_backward_kernel(const NormArgs a, const HT* __restrict__ h_out,
   bool in[V];
   float gp[V][8], gn[V][8];
   let_successor_start();  // it waits for this kernel's end; its launch need not
+  float4* own = reinterpret_cast<float4*>(smem) + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < kWp; ++i) own[i * blockDim.x] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int u = 0; u < V; ++u) {
-    const int v = (u * a.W + warp) * 32 + lane;
-    in[u] = v < a.d8;
-    float w[8];
-    float4* q = reinterpret_cast<float4*>(smem) + threadIdx.x;
-    load_weight(w_post, v, in[u], a.w_offset, w);
-    q[(kWp + 2 * u) * blockDim.x] = make_float4(w[0], w[1], w[2], w[3]);
-    q[(kWp + 2 * u + 1) * blockDim.x] = make_float4(w[4], w[5], w[6], w[7]);
-    load_weight(w_next, v, in[u], a.w_offset, w);
-    q[(kWn + 2 * u) * blockDim.x] = make_float4(w[0], w[1], w[2], w[3]);
-    q[(kWn + 2 * u + 1) * blockDim.x] = make_float4(w[4], w[5], w[6], w[7]);
-#pragma unroll
-    for (int i = 0; i < kWp; ++i) q[i * blockDim.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    in[u] = (u * a.W + warp) * 32 + lane < a.d8;
 #pragma unroll
     for (int j = 0; j < 8; ++j) gp[u][j] = gn[u][j] = 0.f;
   }
@@ -240,6 +232,17 @@ block_norm_backward_kernel(const NormArgs a, const HT* __restrict__ h_out,
   const int step = gridDim.x * groups;
   int t = blockIdx.x * groups + group, turn = 0;
   ahead(t);
+#pragma unroll
+  for (int u = 0; u < V; ++u) {
+    const int v = (u * a.W + warp) * 32 + lane;
+    float w[8];
+    load_weight(w_post, v, in[u], a.w_offset, w);
+    own[(kWp + 2 * u) * blockDim.x] = make_float4(w[0], w[1], w[2], w[3]);
+    own[(kWp + 2 * u + 1) * blockDim.x] = make_float4(w[4], w[5], w[6], w[7]);
+    load_weight(w_next, v, in[u], a.w_offset, w);
+    own[(kWn + 2 * u) * blockDim.x] = make_float4(w[0], w[1], w[2], w[3]);
+    own[(kWn + 2 * u + 1) * blockDim.x] = make_float4(w[4], w[5], w[6], w[7]);
+  }
   for (; t < a.T; t += step, turn ^= 1) {
     float hv[V][8], yv[V][8], q[V][8], u8[V][8];
     const float gt = gate ? gate[t] : 1.f;
