@@ -246,12 +246,6 @@ struct Step {
   bool scaled;
 };
 
-// A lane's values of a block before the step.
-struct Values {
-  float2 g[4], p[4], m[4], v[4];
-  float sm, sv;  // scales of an 8-bit block
-};
-
 template <int W, bool GBF16, bool S8>
 struct Types {
   using G = typename std::conditional<GBF16, __nv_bfloat16, float>::type;
@@ -299,53 +293,67 @@ struct Tile {
   }
 };
 
+// Where a block's values come from: global memory,
 template <int W, bool GBF16, bool S8, bool FULL>
-__device__ __forceinline__ void load_values(const Tile<W, GBF16, S8>& tl, int warp, int lane,
-                                            Values& x) {
-  const Lane<S8> at(warp, lane, tl.n);
-  at.template load<FULL>(tl.g, x.g);
-  at.template load<FULL>(tl.weights(), x.p);
-  at.template load<FULL>(tl.m, x.m);
-  at.template load<FULL>(tl.v, x.v);
-  if constexpr (S8) {
-    x.sm = tl.m_scale[warp];
-    x.sv = tl.v_scale[warp];
+struct Direct {
+  const Tile<W, GBF16, S8>& tl;
+  const Lane<S8> at;
+  __device__ Direct(const Tile<W, GBF16, S8>& tl, int warp, int lane)
+      : tl(tl), at(warp, lane, tl.n) {}
+  __device__ void g(float2 (&x)[4]) const { at.template load<FULL>(tl.g, x); }
+  __device__ void m(float2 (&x)[4]) const { at.template load<FULL>(tl.m, x); }
+  __device__ void v(float2 (&x)[4]) const { at.template load<FULL>(tl.v, x); }
+  __device__ void p(float2 (&x)[4]) const { at.template load<FULL>(tl.weights(), x); }
+  __device__ float2 scales(int warp) const {
+    return make_float2(tl.m_scale[warp], tl.v_scale[warp]);
   }
-}
+  __device__ void done() const {}
+};
 
 // One block of one tensor by one warp.
-template <int W, bool GBF16, bool S8, bool FULL>
+template <int W, bool GBF16, bool S8, bool FULL, class From>
 __device__ __forceinline__ void step_block(const Tile<W, GBF16, S8>& tl, int warp, int lane,
-                                           const Consts& c, const Step& st, Values& x) {
+                                           const Consts& c, const Step& st, From&& from) {
   const Lane<S8> at(warp, lane, tl.n);
   const float decay = fmaf(-st.lr, tl.wd, 1.f), by = -st.lr1;
-  float2 r[4];  // the root to 2^-23 of itself, as the weights need it
+  float2 m[4], v[4], r[4];  // r: the root to 2^-23 of itself, as the weights need it
+  {
+    float2 g[4];
+    from.g(g);
+    from.m(m);
+    from.v(v);
+    float2 scale = make_float2(0.f, 0.f);
+    if constexpr (S8) scale = from.scales(warp);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float2 m = x.m[i], v = x.v[i], g = x.g[i];
-    if constexpr (S8) {
-      m = mulc(m, x.sm);
-      v = mulc(v, x.sv);
-      v = mul2(v, v);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (S8) {
+        m[i] = mulc(m[i], scale.x);
+        v[i] = mulc(v[i], scale.y);
+        v[i] = mul2(v[i], v[i]);
+      }
+      if (st.scaled) g[i] = mulc(g[i], st.gs);
+      m[i] = sum2(mulc(m[i], c.b1), mulc(g[i], c.omb1), c);
+      v[i] = sum2(mulc(v[i], c.b2), mul2(mulc(g[i], c.omb2), g[i]), c);
+      r[i] = make_float2(near_root(v[i].x), near_root(v[i].y));
     }
-    if (st.scaled) g = mulc(g, st.gs);
-    m = sum2(mulc(m, c.b1), mulc(g, c.omb1), c);
-    v = sum2(mulc(v, c.b2), mul2(mulc(g, c.omb2), g), c);
-    r[i] = make_float2(near_root(v.x), near_root(v.y));
-    const float2 den = fma2(r[i], both(st.inv2), both(c.eps));
-    const float2 q = mul2(m, make_float2(reciprocal(den.x), reciprocal(den.y)));
-    x.p[i] = fma2(q, both(by), mulc(x.p[i], decay));
-    x.m[i] = m;
-    x.v[i] = v;
+    float2 p[4];
+    from.p(p);
+    from.done();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 den = fma2(r[i], both(st.inv2), both(c.eps));
+      const float2 q = mul2(m[i], make_float2(reciprocal(den.x), reciprocal(den.y)));
+      p[i] = fma2(q, both(by), mulc(p[i], decay));
+    }
+    at.template store<FULL>(tl.p, p);
+    if constexpr (W == W_BF16_MASTER) at.template store<FULL>(tl.master, p);
   }
-  at.template store<FULL>(tl.p, x.p);
-  if constexpr (W == W_BF16_MASTER) at.template store<FULL>(tl.master, x.p);
   if constexpr (S8) {
     float top_m = 0.f, top_v = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      top_m = top3(x.m[i].x, x.m[i].y, top_m);
-      top_v = top3(x.v[i].x, x.v[i].y, top_v);
+      top_m = top3(m[i].x, m[i].y, top_m);
+      top_v = top3(v[i].x, v[i].y, top_v);
     }
     top_m = warp_top(top_m);
     top_v = warp_top(top_v);  // the nearest root rises with v: the largest root is its
@@ -358,7 +366,7 @@ __device__ __forceinline__ void step_block(const Tile<W, GBF16, S8>& tl, int war
     float least = INFINITY;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x.m[i] = mulc(x.m[i], im);
+      m[i] = mulc(m[i], im);
       r[i] = mulc(r[i], ir);
       // The code goes by the nearest root.  This one, and its product, are off by 4 steps at
       // most, which matters only next to a border between codes (half way in the last 20
@@ -370,19 +378,19 @@ __device__ __forceinline__ void step_block(const Tile<W, GBF16, S8>& tl, int war
     if ((border <= 16u || least < 0.015625f) && ir > 0.f) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        r[i] = make_float2(__fmul_rn(__fsqrt_rn(x.v[i].x), ir),
-                           __fmul_rn(__fsqrt_rn(x.v[i].y), ir));
-        if (x.v[i].x > 0.f) r[i].x = fmaxf(r[i].x, kE4m3Tiny);
-        if (x.v[i].y > 0.f) r[i].y = fmaxf(r[i].y, kE4m3Tiny);
+        r[i] = make_float2(__fmul_rn(__fsqrt_rn(v[i].x), ir),
+                           __fmul_rn(__fsqrt_rn(v[i].y), ir));
+        if (v[i].x > 0.f) r[i].x = fmaxf(r[i].x, kE4m3Tiny);
+        if (v[i].y > 0.f) r[i].y = fmaxf(r[i].y, kE4m3Tiny);
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x.v[i] = r[i];
+    for (int i = 0; i < 4; ++i) v[i] = r[i];
     if (lane < 2)
       (lane ? tl.v_scale : tl.m_scale)[warp] = some ? __fmul_rn(top, 1.f / kE4m3Max) : 0.f;
   }
-  at.template store<FULL>(tl.m, x.m);
-  at.template store<FULL>(tl.v, x.v);
+  at.template store<FULL>(tl.m, m);
+  at.template store<FULL>(tl.v, v);
 }
 
 // 16-byte slots of a thread, kThreads apart: the next block's gradient, weights and codes.
@@ -406,6 +414,14 @@ struct Ahead {
     sm = tl.m_scale[warp];
     sv = tl.v_scale[warp];
   }
+  __device__ uint2 codes(uint32_t byte) const {
+    uint2 a;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(a.x), "=r"(a.y)
+                 : "r"(slot + (kG + kP) * kPitch + byte)
+                 : "memory");
+    return a;
+  }
   template <int UNITS>
   __device__ void read(int unit, float2 (&v)[4]) const {
     const uint4 a = slot16(slot + unit * kPitch);
@@ -421,19 +437,35 @@ struct Ahead {
       v[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
     }
   }
-  __device__ void take(Values& x) const {
-    read<kG>(0, x.g);
-    read<kP>(kG, x.p);
-    const uint4 a = slot16(slot + (kG + kP) * kPitch);
-    decode8(a.x, a.y, x.m);
-    decode8(a.z, a.w, x.v);
-    x.sm = sm;
-    x.sv = sv;
+};
+// or the slots, which take the next block as soon as they have been read.
+template <int W, bool GBF16, int CAP>
+struct Copied {
+  Ahead<W, GBF16>& from;
+  const Batch<CAP>& b;
+  int next_item, next_tile, warp, lane;
+  __device__ void g(float2 (&x)[4]) const { from.template read<Ahead<W, GBF16>::kG>(0, x); }
+  __device__ void p(float2 (&x)[4]) const {
+    from.template read<Ahead<W, GBF16>::kP>(Ahead<W, GBF16>::kG, x);
+  }
+  __device__ void m(float2 (&x)[4]) const {
+    const uint2 a = from.codes(0);
+    decode8(a.x, a.y, x);
+  }
+  __device__ void v(float2 (&x)[4]) const {
+    const uint2 a = from.codes(8);
+    decode8(a.x, a.y, x);
+  }
+  __device__ float2 scales(int) const { return make_float2(from.sm, from.sv); }
+  __device__ void done() const {
+    const Tile<W, GBF16, true> next(b, next_item, next_tile);
+    if (next.n == kTile) from.fill(next, warp, lane);
+    commit_copies();
   }
 };
 
 template <int W, bool GBF16, bool S8, int CAP>
-__global__ void __launch_bounds__(kThreads, S8 ? 3 : 4)
+__global__ void __launch_bounds__(kThreads, S8 && W != W_BF16 ? 3 : 4)
 adamw_kernel(const __grid_constant__ Batch<CAP> b, const __grid_constant__ Consts c,
              const float* lr_p, const float* grad_scale, int32_t* step, bool last_launch) {
   __shared__ __align__(16) char smem[S8 ? Ahead<W, GBF16>::kBytes : 16];
@@ -470,21 +502,24 @@ adamw_kernel(const __grid_constant__ Batch<CAP> b, const __grid_constant__ Const
     int next_item = next < tiles ? item : b.count;
     while (next_item < b.count && b.first_tile[next_item + 1] <= next) ++next_item;
     const Tile<W, GBF16, S8> tl(b, item, tile);
-    Values x;
+    // a tensor's last tile: block by block, each lane looking after its own elements
     if constexpr (S8) {
       wait_copies<0>();
-      if (tl.n == kTile) ahead.take(x);
-      const Tile<W, GBF16, S8> nx(b, next_item, next);
-      if (nx.n == kTile) ahead.fill(nx, warp, lane);
-      commit_copies();
-    }
-    // a tensor's last tile: block by block, each lane looking after its own elements
-    if (tl.n == kTile) {
-      if constexpr (!S8) load_values<W, GBF16, S8, true>(tl, warp, lane, x);
-      step_block<W, GBF16, S8, true>(tl, warp, lane, c, st, x);
+      const Copied<W, GBF16, CAP> copied = {ahead, b, next_item, next, warp, lane};
+      if (tl.n == kTile) {
+        step_block<W, GBF16, S8, true>(tl, warp, lane, c, st, copied);
+      } else {
+        copied.done();
+        if (warp * kBlock < tl.n)
+          step_block<W, GBF16, S8, false>(tl, warp, lane, c, st,
+                                          Direct<W, GBF16, S8, false>(tl, warp, lane));
+      }
+    } else if (tl.n == kTile) {
+      step_block<W, GBF16, S8, true>(tl, warp, lane, c, st,
+                                     Direct<W, GBF16, S8, true>(tl, warp, lane));
     } else if (warp * kBlock < tl.n) {
-      load_values<W, GBF16, S8, false>(tl, warp, lane, x);
-      step_block<W, GBF16, S8, false>(tl, warp, lane, c, st, x);
+      step_block<W, GBF16, S8, false>(tl, warp, lane, c, st,
+                                      Direct<W, GBF16, S8, false>(tl, warp, lane));
     }
     tile = next;
     item = next_item;

@@ -59,6 +59,13 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
+// With 32-byte alignment a lane's 8 values leave in one store of a whole sector; in two, each
+// store of the warp touches every sector and fills half of it.
+__device__ __forceinline__ void store8_whole(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&t);
@@ -67,6 +74,13 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
   *reinterpret_cast<uint4*>(p) =
       make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                  pack_bf16x2(v[6], v[7]));
+}
+
+__device__ __forceinline__ void store8_whole(__nv_bfloat16* p, const float* v) { store8(p, v); }
+template <class T>
+__device__ __forceinline__ void store8_if(bool whole, T* p, const float* v) {
+  if (whole) store8_whole(p, v);
+  else store8(p, v);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -80,8 +94,8 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// ---- a thread's own copies ahead of time: 16 bytes from global to its shared-memory slots,
-// read back by the same thread after wait_copies() (so no barrier guards them) ----
+// ---- copies ahead of time, 16 (or 8) bytes from global to shared memory, read back by the
+// thread that made them after wait_copies() (so no barrier guards them) ----
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
