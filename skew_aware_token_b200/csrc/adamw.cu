@@ -4,20 +4,25 @@
 //   p = p (1 - lr wd) - (lr / (1 - b1^t)) m / (sqrt(v) / sqrt(1 - b2^t) + eps).
 //
 // The tensors' addresses travel in the launch's parameters, so a call needs neither a table in
-// device memory nor a copy to one.  Tensors of one combination of types share a launch; a
-// persistent grid walks their tiles of 2048 elements (a warp per block of 256: each lane
-// holds elements 4 l .. 4 l + 3 of either half, so every load and store is a run of whole
-// sectors) and finds a tile's tensor by bisection of the tile prefix.
+// device memory nor a copy to one.  Tensors of one combination of types share a launch, whose
+// CTAs take tiles of 2048 elements (a warp per block of 256) at the grid's stride; a CTA finds
+// its first tile's tensor by bisection and steps on from there.
 //
 // 8-bit moments hold a block of 256 elements as e4m3 with one fp32 scale: m itself, and the
 // root r of v (whose range is half of v's in the exponent: e4m3's 2^18 of range for r is
-// 2^36 for v).  The new largest |m| and r of a block are two warp reductions of the bit
-// patterns (non-negative floats order as integers).  The moments' operations and the
-// roundings to codes are the IEEE ones, each rounded by itself, so the stored states are
-// reproducible outside this kernel bit for bit; the weight's quotient is the approximate one
-// (2 ulp of fp32, below what the weight's own rounding does to it).
+// 2^36 for v).  A block's largest |m| and v are two warp reductions of the bit patterns
+// (non-negative floats order as integers).  The moments, the scales and the roundings to
+// codes are those of IEEE operations, each rounded by itself, so the stored states are
+// reproducible outside this kernel bit for bit; the weight's root and quotient are
+// approximate ones (a few steps of fp32, below what the weight's own rounding does).
 //
-// Bound by HBM: 4 (p) + 4 (g) + 4 (m, v) bytes an element with bf16 weights and 8-bit states.
+// Bound by HBM: fp32 states 200 us for 50 M fp32 weights with bf16 gradients (26 bytes each,
+// 6.5 TB/s, a copy's rate).  With bf16 weights, fp32 gradients and 8-bit states 12 bytes an
+// element carry 46 instructions: 402 M weights take 850 us at first and 925 us once the power
+// limit has lowered the clocks (4.86 GB: 741 us at a copy's rate).  The same accesses without
+// the arithmetic take 810 to 830 us, so what is left above them is the arithmetic that they
+// do not hide; streaming stores, wider or narrower CTAs and two or four blocks a warp gave
+// nothing or cost time.
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -56,7 +61,7 @@ struct Batch {
   int32_t first_tile[CAP + 1];
   Item item[CAP];
 };
-constexpr int kCaps[3] = {8, 64, 400};
+constexpr int kCaps[3] = {8, 128, 400};
 static_assert(sizeof(Batch<400>) <= 32000, "launch parameters");
 
 struct Consts {

@@ -131,7 +131,7 @@ router_backward_kernel(const RouterArgs a, const float* __restrict__ logits,
       }
       if (on) {
         const float n_s = (float)seq_info[seq];
-        const float scale = b / (n_s * n_s);
+        const float scale = n_s > 0.f ? b / (n_s * n_s) : 0.f;
 #pragma unroll
         for (int i = 0; i < kEpt; ++i) {
           const int e = tid + i * 32 * W;

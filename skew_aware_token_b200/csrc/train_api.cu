@@ -1,5 +1,6 @@
 // C ABI of the training operators: argument validation, then the launchers.  Nothing is
 // enqueued when validation fails; see include/moeskew_train.h for the contract.
+#include <cfloat>
 #include <cmath>
 #include <initializer_list>
 
@@ -134,7 +135,7 @@ int moet_adamw_step(const moet_adamw_tensor* tensors, int32_t count, const moet_
                     moe_stream_t stream) {
   if (count < 0 || (count > 0 && !tensors) || !opt) return MOE_ERR_INVALID_ARG;
   if (!(opt->beta1 >= 0. && opt->beta1 < 1.) || !(opt->beta2 >= 0. && opt->beta2 < 1.) ||
-      !(opt->eps >= 0.) || !std::isfinite(opt->eps))
+      !((float)opt->eps >= FLT_MIN) || !std::isfinite((float)opt->eps))
     return MOE_ERR_INVALID_ARG;
   int rc = check_ptrs({lr, step});
   if (rc == MOE_OK) rc = check_optional({grad_scale});

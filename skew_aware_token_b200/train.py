@@ -297,8 +297,8 @@ class AdamW(_OnDevice):
             raise ValueError("no parameters")
         if state_bits not in (8, 32):
             raise ValueError("state_bits is 8 or 32")
-        if not all(0 <= b < 1 for b in betas) or not eps >= 0 or step < 0:
-            raise ValueError("betas in [0, 1), eps >= 0 and step >= 0 are needed")
+        if not all(0 <= b < 1 for b in betas) or not eps > 0 or step < 0:
+            raise ValueError("betas in [0, 1), eps > 0 and step >= 0 are needed")
         first = self.params[0]
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise TypeError("params must be CUDA tensors")

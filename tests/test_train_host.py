@@ -174,8 +174,9 @@ def test_adamw_refusals():
                 dict(state_dtype=1), dict(weight_decay=float("nan"))):
         assert go(tensors(**bad)) == INVALID, bad
     assert go(tensors(n=(1 << 40) + 1)) == UNSUPPORTED
-    for bad in ((1.0, 0.9, 0.0), (-0.1, 0.9, 0.0), (0.9, 1.0, 0.0), (0.9, 0.9, -1.0),
-                (float("nan"), 0.9, 0.0), (0.9, 0.9, float("inf"))):
+    for bad in ((1.0, 0.9, 1e-8), (-0.1, 0.9, 1e-8), (0.9, 1.0, 1e-8), (0.9, 0.9, 0.0),
+                (0.9, 0.9, -1.0), (0.9, 0.9, 1e-40), (float("nan"), 0.9, 1e-8),
+                (0.9, 0.9, float("inf"))):
         assert go(o=N.MoetAdamw(*bad)) == INVALID, bad
     assert go(lr=None) == INVALID and go(st=None) == INVALID
     assert go(lr=OK + 4) == UNSUPPORTED and go(gs=OK + 4) == UNSUPPORTED
