@@ -270,6 +270,14 @@ _SIGNATURES.update({
 })
 
 
+def call(fn: str, *args) -> None:
+    """Entry point `fn` on addresses that its caller has checked (ctypes structures by
+    reference, the stream's handle last); raises as the wrappers do."""
+    rc = getattr(_lib or lib(), fn)(*args)
+    if rc != MOE_OK:
+        raise MoeError(fn, rc)
+
+
 def moet_workspace_size(cfg, n_seq: int, which: int) -> int:
     return int(lib().moet_workspace_size(ctypes.byref(_cfg(cfg)), n_seq, which))
 

@@ -44,52 +44,56 @@ def _device(device) -> torch.device:
     return torch.device("cuda", torch.cuda.current_device()) if dev.index is None else dev
 
 
-def _need(t, name, dtype, n, dev, optional=False):
+def _need(t, name, dtype, n, index, optional=False):
     """The address of one array argument, after its checks: a contiguous tensor of `dtype` on
-    `dev` with `n` elements, or a flat buffer of at least that many (what MoeLayer owns).
-    None when it is left out."""
+    CUDA device `index` with `n` elements, or a flat buffer of at least that many (what
+    MoeLayer owns).  None when it is left out."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n and \
+            t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
     if t is None:
         if optional:
             return None
         raise TypeError(f"{name} is needed")
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n and \
-            t.get_device() == dev.index and t.is_contiguous():
-        return t.data_ptr()
     # what is wrong with it, or a flat buffer
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev.index:
-        raise TypeError(f"{name} must be a tensor on {dev}")
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        raise TypeError(f"{name} must be a tensor on cuda:{index}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    have = t.numel()
-    if not t.is_contiguous() or (have != n and (have < n or t.dim() != 1)):
+    if not t.is_contiguous() or t.numel() < n or t.dim() != 1:
         raise ValueError(f"{name} must be contiguous with {n} elements")
     return t.data_ptr()
 
 
-# The current stream's handle without a Stream object around it (a fifth of a small call).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _current_stream(dev) -> int:
-    if _raw_stream is not None:
-        return _raw_stream(dev.index)
-    return torch.cuda.current_stream(dev).cuda_stream
+# The current device and its current stream's handle without the objects around them (a fifth
+# of a small call's time).
+_device_index = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class _OnDevice:
     """Runs a call with the object's device current and the stream resolved on it."""
 
-    def _call(self, fn, *args, stream=None):
-        dev = self.device
+    def _on(self, device):
+        self.device = device
+        self._index = device.index
+
+    def _call(self, fn, args, stream):
+        index = self._index
         if stream is None:
-            stream = _current_stream(dev)
-        elif isinstance(stream, torch.cuda.Stream) and stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the arrays on {dev}")
-        if torch.cuda.current_device() == dev.index:
-            fn(*args, stream=stream)
+            stream = _raw_stream(index)
+        elif isinstance(stream, torch.cuda.Stream):
+            if stream.device != self.device:
+                raise ValueError(f"the stream is on {stream.device}, the arrays on {self.device}")
+            stream = stream.cuda_stream
         else:
-            with torch.cuda.device(dev):
-                fn(*args, stream=stream)
+            stream = int(stream)
+        if _device_index() == index:
+            N.call(fn, *args, stream)
+        else:
+            with torch.cuda.device(index):
+                N.call(fn, *args, stream)
 
 
 class RouterLoss(_OnDevice):
@@ -102,7 +106,9 @@ class RouterLoss(_OnDevice):
         size = N.moet_workspace_size(self.cfg, self.n_seq, N.MOET_WS_BALANCE)
         if size == 0:
             raise ValueError("configuration or n_seq rejected by moet_workspace_size")
-        dev = self.device = _device(device)
+        dev = _device(device)
+        self._on(dev)
+        self._cfg = ctypes.byref(self.cfg)
         T, E, k, S = self.cfg.T, self.cfg.E, self.cfg.k, self.n_seq
         z = lambda *shape, dt=torch.float32: torch.zeros(shape, dtype=dt, device=dev)
         self.losses = z(2)
@@ -124,22 +130,25 @@ class RouterLoss(_OnDevice):
         self._grads = [t.data_ptr() for t in (self._dgates, self._dlogits, self.status)]
 
     def _batch(self, token_mask, seq_off):
-        return (_need(token_mask, "token_mask", torch.uint8, self.cfg.T, self.device, True),
-                _need(seq_off, "seq_off", torch.int32, self.n_seq + 1, self.device,
-                      self.n_seq == 1))
+        mask = off = None
+        if token_mask is not None:
+            mask = _need(token_mask, "token_mask", torch.uint8, self.cfg.T, self._index)
+        if seq_off is not None or self.n_seq != 1:
+            off = _need(seq_off, "seq_off", torch.int32, self.n_seq + 1, self._index)
+        return mask, off
 
     def __call__(self, logits, topk_ids, token_mask=None, seq_off=None, stream=None):
         """fp32 [2]: balance loss and z loss of logits fp32 [T, E] and the router's topk_ids
         int32 [T, k].  token_mask uint8 [T] leaves tokens out; seq_off int32 [n_seq + 1] are
         the sequences' bounds (None with one sequence: the whole batch)."""
-        c, dev = self.cfg, self.device
+        c, dev = self.cfg, self._index
         x = _need(logits, "logits", torch.float32, c.T * c.E, dev)
         ids = _need(topk_ids, "topk_ids", torch.int32, c.T * c.k, dev)
         mask, off = self._batch(token_mask, seq_off)
         if c.T == 0:  # empty tensors have no address
             x, ids, mask = self._grads[1], self._grads[1], None
-        self._call(N.moet_balance_loss, c, x, ids, mask, off, self.n_seq, *self._outputs,
-                   stream=stream)
+        self._call("moet_balance_loss",
+                   (self._cfg, x, ids, mask, off, self.n_seq, *self._outputs), stream)
         return self.losses
 
     def backward(self, logits=None, topk_ids=None, topk_gates=None, dloss=None, dy=None, o=None,
@@ -148,7 +157,7 @@ class RouterLoss(_OnDevice):
         the forward call on the same logits, ids, mask and sequences), the gates' part with
         dy (fp32 [T, d]), o (the expert output rows, bf16 [R_max, d]) and tok_row, or both.
         The gates' gradient is in `dgates` then."""
-        c, dev = self.cfg, self.device
+        c, dev = self.cfg, self._index
         gates = dy is not None or o is not None or tok_row is not None
         if not gates and dloss is None:
             raise ValueError("nothing to take the gradient of: give dloss, or dy, o and tok_row")
@@ -166,8 +175,9 @@ class RouterLoss(_OnDevice):
         if c.T == 0:
             return self.dlogits
         dgates, dlogits, status = self._grads
-        self._call(N.moet_router_backward, c, x, ids, g, dy_p, o_p, row, mask, off, self.n_seq,
-                   *self._saved, dl, dgates if gates else None, dlogits, status, stream=stream)
+        self._call("moet_router_backward",
+                   (self._cfg, x, ids, g, dy_p, o_p, row, mask, off, self.n_seq, *self._saved, dl,
+                    dgates if gates else None, dlogits, status), stream)
         return self.dlogits
 
     def clear_status(self):
@@ -201,7 +211,8 @@ class BlockNorm(_OnDevice):
         if size == 0:
             raise ValueError("configuration rejected by moet_workspace_size (d % 8 == 0 and "
                              f"d <= {N.MOET_MAX_NORM_D} are needed)")
-        dev = self.device = _device(device)
+        dev = _device(device)
+        self._on(dev)
         T, d = self.cfg.T, self.cfg.d
         self.h_dtype, self.w_dtype, self.train = h_dtype, w_dtype, bool(train)
         self.norm = N.MoetNorm(eps, w_offset, res_scale, out_scale, _TYPES[h_dtype],
@@ -214,14 +225,15 @@ class BlockNorm(_OnDevice):
             self.dgate = new(torch.float32, rows)[:T]
             self.dw_post, self.dw_next = new(torch.float32, d), new(torch.float32, d)
             self.workspace = new(torch.uint8, size)
+        self._refs = (ctypes.byref(self.cfg), ctypes.byref(self.norm))
 
     def _inputs(self, h, y, gate, w_post, w_next):
-        T, d, dev = self.cfg.T, self.cfg.d, self.device
+        T, d, dev = self.cfg.T, self.cfg.d, self._index
         if y is None and (gate is not None or w_post is not None):
             raise ValueError("gate and w_post belong to y")
         return (_need(h, "h", self.h_dtype, T * d, dev),
                 _need(y, "y", torch.float32, T * d, dev, True),
-                _need(gate, "gate", torch.float32, T, dev, True),
+                None if gate is None else _need(gate, "gate", torch.float32, T, dev),
                 _need(w_post, "w_post", self.w_dtype, d, dev, True),
                 _need(w_next, "w_next", self.w_dtype, d, dev, True))
 
@@ -239,11 +251,11 @@ class BlockNorm(_OnDevice):
             to = None
         else:
             h_out = self.h_out if h_out is None else h_out
-            to = _need(h_out, "h_out", self.h_dtype, c.T * c.d, self.device)
+            to = _need(h_out, "h_out", self.h_dtype, c.T * c.d, self._index)
         x = None if w_next is None else self.x
         if c.T:
-            self._call(N.moet_block_norm, c, self.norm, *inputs, to,
-                       None if x is None else x.data_ptr(), stream=stream)
+            self._call("moet_block_norm", (*self._refs, *inputs, to,
+                                           None if x is None else x.data_ptr()), stream)
         return (h if y is None else h_out), x
 
     def backward(self, h_out, y=None, gate=None, w_post=None, w_next=None, dh_out=None, dx=None,
@@ -254,7 +266,7 @@ class BlockNorm(_OnDevice):
         if not self.train:
             raise ValueError("built without train=True")
         c = self.cfg
-        T, d, dev = c.T, c.d, self.device
+        T, d, dev = c.T, c.d, self._index
         inputs = self._inputs(h_out, y, gate, w_post, w_next)
         into = (_need(dh_out, "dh_out", self.h_dtype, T * d, dev, True),
                 _need(dx, "dx", torch.float32, T * d, dev, True))
@@ -266,9 +278,10 @@ class BlockNorm(_OnDevice):
         g = BlockNormGrads(self.dh, only(self.dy, y), only(self.dgate, gate),
                            only(self.dw_post, w_post), only(self.dw_next, w_next))
         if T:
-            self._call(N.moet_block_norm_backward, c, self.norm, *inputs, *into,
-                       *[None if t is None else t.data_ptr() for t in g],
-                       self.workspace.data_ptr(), stream=stream)
+            self._call("moet_block_norm_backward",
+                       (*self._refs, *inputs, *into,
+                        *[None if t is None else t.data_ptr() for t in g],
+                        self.workspace.data_ptr()), stream)
         else:
             for dw in (g.dw_post, g.dw_next):
                 if dw is not None:
@@ -302,7 +315,8 @@ class AdamW(_OnDevice):
         first = self.params[0]
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise TypeError("params must be CUDA tensors")
-        dev = self.device = first.device
+        dev = first.device
+        self._on(dev)
         count = len(self.params)
         decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else \
             [float(weight_decay)] * count
@@ -332,7 +346,7 @@ class AdamW(_OnDevice):
         for i, p in enumerate(self.params):
             if p.dtype not in (torch.float32, torch.bfloat16):
                 raise TypeError("params must be torch.float32 or torch.bfloat16")
-            _need(p, f"params[{i}]", p.dtype, sizes[i], dev)
+            _need(p, f"params[{i}]", p.dtype, sizes[i], dev.index)
             own = [("m", self.m[i], state, sizes[i]), ("v", self.v[i], state, sizes[i])]
             if state_bits == 8:
                 own += [("m_scale", self.m_scale[i], torch.float32, blocks[i]),
@@ -343,7 +357,7 @@ class AdamW(_OnDevice):
                     raise ValueError("fp32 weights have no master")
                 own.append(("master", w, torch.float32, sizes[i]))
             for name, t, dt, n in own:
-                _need(t, f"{name}[{i}]", dt, n, dev)
+                _need(t, f"{name}[{i}]", dt, n, dev.index)
             for name, t, dt, n in own + [("params", p, p.dtype, sizes[i])]:
                 if n:
                     spans.append((t.data_ptr(), t.data_ptr() + n * t.element_size(),
@@ -400,6 +414,7 @@ class AdamW(_OnDevice):
                 not all(map(torch.Tensor.is_contiguous, grads)):
             raise ValueError("grads must be contiguous and of their parameters' sizes")
         self._g[:] = array.array("Q", map(torch.Tensor.data_ptr, grads))
-        scale = _need(grad_scale, "grad_scale", torch.float32, 1, self.device, True)
-        self._call(N.moet_adamw_step, self._tensors, len(grads), self._opt, self.lr, scale,
-                   self.steps, stream=stream)
+        scale = _need(grad_scale, "grad_scale", torch.float32, 1, self._index, True)
+        self._call("moet_adamw_step",
+                   (self._tensors, len(grads), ctypes.byref(self._opt), self.lr.data_ptr(),
+                    scale, self.steps.data_ptr()), stream)

@@ -487,6 +487,25 @@ def test_adamw(bits, pt, master, gt):
                   (2.0 ** -4 + 16 * U) * v.sqrt() + 2.0 ** -9 * sc, "root of v")
 
 
+@pytest.mark.parametrize("spread", [1.0, 8.0, 30.0])
+def test_adamw_codes_of_many_roots(spread):
+    """Four million roots, spread over up to 2^30 within a block (most of e4m3's codes, its
+    subnormal ones, roots far below them, zeros): the nearest codes bit for bit.  About 60 of
+    the roots lie within a few fp32 steps of a border between two codes."""
+    n = 1 << 22
+    g = torch.randn(n, generator=gen(1)) * torch.exp2(-spread * torch.rand(n, generator=gen(2)))
+    g[::97] = 0
+    opt = AdamW([torch.zeros(n, device=DEV)], lr=LR, betas=(B1, B2), state_bits=8)
+    opt.step([g.to(DEV)])
+    f = lambda t: torch.tensor(t, dtype=torch.float32)
+    m32, v32 = g * f(1 - B1), (g * f(1 - B2)) * g
+    for got, s, (want, ws) in ((opt.m[0], opt.m_scale[0], R.to_8bit(m32, False)),
+                               (opt.v[0], opt.v_scale[0],
+                                R.to_8bit(v32.double().sqrt().float(), True))):
+        assert torch.equal(s.cpu(), ws)
+        assert torch.equal(got.cpu().view(torch.uint8), want.view(torch.uint8))
+
+
 def test_adamw_scale_skip_and_mixed_tensors():
     """grad_scale multiplies; a scale that is not finite leaves the step out; tensors of every
     kind and more of them than one launch holds step together."""
