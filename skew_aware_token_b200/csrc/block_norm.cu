@@ -3,16 +3,21 @@
 //   n(v; w) = v * rms(v) * (w + w_offset),  rms(v) = rsqrt(mean(v^2) + eps)
 //   h' = res_scale h + out_scale g n(y; w_post),   x = bf16(n(h'; w_next))
 //
-// One pass: a row lives in the registers of a group of warps (8 columns a thread and step),
+// One pass: a row lives in the registers of a group of warps (units of 4 columns, two a thread),
 // so h, y and the weights are read once and h' and x are written once; the two means are two
-// reductions over the group.  Bound by HBM.
+// reductions over the group.  A persistent group copies its next row to shared memory while it
+// works on this one.  Bound by HBM: 16384 x 7168 with an fp32 stream 265 us (1.64 GB, 6.2
+// TB/s; a copy of as many bytes takes 251), 4096 x 2048 in bf16 17 us (12.8).
 //
 // The gradient needs six sums of a row, and by linearity one reduction for all of them: with
 // q = dx (w_next + o), u = dh' + A q - B h', A = rms(h'), B = A^3 <q, h'> / d,
 //   <u w_post, y> = <dh' w_post, y> + A <q w_post, y> - B <h' w_post, y>,
-// so u itself is not needed before the reduction.  The weights' gradients are kept per column
-// in registers over all rows of a CTA, written as one partial row per CTA, and added over
-// the CTAs in a fixed order by a second kernel.
+// so u itself is not needed before the reduction (nine shuffles for all six).  The weights'
+// gradients are kept per column in registers over all rows of a CTA, written as one partial
+// row per CTA, and added over the CTAs in a fixed order by a second kernel.  128 registers a
+// thread without a spill: a few spilled ones in the row loop cost half of the rate.
+// 16384 x 7168 in bf16 takes 361 us (2.11 GB, 5.9 TB/s; a copy of as many bytes 323); what it
+// waits for most are shared memory and the reduction's shuffles.
 #include "train_common.cuh"
 
 namespace moe {
@@ -22,56 +27,101 @@ namespace {
 // holds, four per SM of a 148-SM GPU.
 constexpr int kMaxPartials = 592;
 
-constexpr int kFwdThreads = 512;  // of a CTA with several row groups
-
 struct NormArgs {
-  int T, d8, W;  // rows, 8-column steps of a row, warps of a row's group
+  int T, d4, W;  // rows, 4-column units of a row, warps of a row's group
   float inv_d, eps, w_offset, res_scale, out_scale;
-  bool whole;  // the fp32 outputs lie on 32 bytes
 };
 
+// ---- units of 4 columns: of bf16 8 bytes, of fp32 16.  Consecutive lanes take consecutive
+// units, so every copy, load and store of a warp is one run of whole sectors ----
+__device__ __forceinline__ void load4(const float* p, float* v) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* v) {
+  const uint2 a = *reinterpret_cast<const uint2*>(p);
+  v[0] = __uint_as_float(a.x << 16), v[1] = __uint_as_float(a.x & 0xffff0000u);
+  v[2] = __uint_as_float(a.y << 16), v[3] = __uint_as_float(a.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
 template <class WT>
-__device__ __forceinline__ void load_weight(const WT* w, int v, bool in, float offset,
+__device__ __forceinline__ void load_weight(const WT* w, int unit, bool in, float offset,
                                             float* out) {
   if (w && in) {
-    load8(w + v * 8, out);
+    load4(w + unit * 4, out);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) out[j] += offset;
+    for (int j = 0; j < 4; ++j) out[j] += offset;
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) out[j] = 1.f;
+    for (int j = 0; j < 4; ++j) out[j] = 1.f;
   }
 }
 
-// The 8 elements of a lane in its slots: one 16-byte unit of bf16 or two of fp32, units a CTA's
-// width apart (consecutive lanes read consecutive 16 bytes).  A lane copies and reads its own
-// slots, so no barrier guards them.  The copies go through L1, where the second half of an
-// fp32 sector hits: past L1, or with the warp's copies rearranged to runs of 512 bytes, the
-// 16384 x 7168 forward took 407 and 295 us for 286.
+// A unit's slot in shared memory, and the unit as it is stored (a bf16 one takes half the
+// registers while it waits for its row's sums).  A lane copies and reads its own slots, so no
+// barrier guards them; the copies go through L1 (past it they took a third longer).
 template <class T>
-struct Slots {
-  static constexpr int kUnits = sizeof(T) * 8 / 16;
-  __device__ static void fill(uint32_t slot, uint32_t pitch, const T* src) {
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i)
-      copy_ahead16(slot + i * pitch, reinterpret_cast<const char*>(src) + 16 * i);
+struct Unit;
+template <>
+struct Unit<float> {
+  static constexpr int kBytes = 16;
+  float v[4];
+  __device__ static void copy(uint32_t slot, const float* src) { copy_ahead16(slot, src); }
+  __device__ static void clear(uint32_t slot) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(slot), "r"(0) : "memory");
   }
-  __device__ static void read(uint32_t slot, uint32_t pitch, float* v) {
-    if constexpr (kUnits == 1) {
-      bf16x8_to_f32(slot16(slot), v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 a = slot16(slot + i * pitch);
-        v[4 * i] = __uint_as_float(a.x), v[4 * i + 1] = __uint_as_float(a.y);
-        v[4 * i + 2] = __uint_as_float(a.z), v[4 * i + 3] = __uint_as_float(a.w);
-      }
-    }
+  __device__ void read(uint32_t slot) {
+    const uint4 a = slot16(slot);
+    v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y);
+    v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
+  }
+  __device__ float operator[](int j) const { return v[j]; }
+};
+template <>
+struct Unit<__nv_bfloat16> {
+  static constexpr int kBytes = 8;
+  uint32_t w[2];
+  __device__ static void copy(uint32_t slot, const __nv_bfloat16* src) {
+    copy_ahead8(slot, src);
+  }
+  __device__ static void clear(uint32_t slot) {
+    asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(slot), "r"(0) : "memory");
+  }
+  __device__ void read(uint32_t slot) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(w[0]), "=r"(w[1])
+                 : "r"(slot)
+                 : "memory");
+  }
+  __device__ float operator[](int j) const {
+    return __uint_as_float(j % 2 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
   }
 };
 
-// The sum over the group of one value, on every thread.  `red` is one of the group's buffers of
-// 32 floats; a caller uses two in turn, so one barrier a sum is enough.
+// The slots of one array: kUnits units a thread.
+template <class T>
+struct Array {
+  uint32_t first, pitch;
+  __device__ Array(uint32_t base, int threads)
+      : first(base + threadIdx.x * Unit<T>::kBytes), pitch(threads * Unit<T>::kBytes) {}
+  __device__ uint32_t slot(int i) const { return first + i * pitch; }
+};
+
+// Units of a thread, its columns of every row of its group.  Forward: 2, so that the weights
+// stay in registers with 32 warps a row.  Backward: 4, since its reduction of six sums costs
+// a thread the same whatever it holds.
+constexpr int kFwdUnits = 2, kBwdUnits = 4;
+constexpr int kThreads = 512;       // of a CTA with several row groups, or of the backward's
+constexpr int kFwdRed = 2 * 32;     // floats of a group's reduction buffers
+constexpr int kBwdRed = 2 * 8 * 17;
+
+// The sum over the group of one value, on every thread.  `red` is one of the group's buffers;
+// a caller uses two in turn, so one barrier a sum is enough.
 __device__ __forceinline__ float group_sum(float v, int W, int group, int warp, int lane,
                                            float* red) {
   v = warp_sum(v);
@@ -79,105 +129,6 @@ __device__ __forceinline__ float group_sum(float v, int W, int group, int warp, 
   if (lane == 0) red[warp] = v;
   asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(W * 32) : "memory");
   return warp_sum(lane < W ? red[lane] : 0.f);
-}
-
-// A thread owns 8 columns of every row of its group, and their weights.  The next row's
-// columns are copied to the thread's slots as soon as this row's are in registers, so that
-// memory works through both means of a row (two or three rows ahead gave nothing: they only
-// take L1 from the copies).
-template <class HT, class WT>
-__global__ void __launch_bounds__(1024)
-block_norm_kernel(const NormArgs a, const HT* h, const float* __restrict__ y,
-                  const float* __restrict__ gate, const WT* __restrict__ w_post,
-                  const WT* __restrict__ w_next, HT* h_out, __nv_bfloat16* __restrict__ x) {
-  constexpr int HU = Slots<HT>::kUnits;
-  extern __shared__ __align__(16) char smem[];
-  const int lane = threadIdx.x & 31;
-  const int group = (threadIdx.x >> 5) / a.W, warp = (threadIdx.x >> 5) % a.W;
-  const int groups = (blockDim.x >> 5) / a.W;
-  const uint32_t pitch = blockDim.x * 16;
-  const uint32_t slot_h = smem_addr(smem) + threadIdx.x * 16, slot_y = slot_h + HU * pitch;
-  float* red = reinterpret_cast<float*>(smem + (HU + 2) * pitch) + group * 64;
-  const int v = warp * 32 + lane;
-  const bool in = v < a.d8;
-  auto ahead = [&](int t) {
-    if (t < a.T && in) {
-      const long long at = ((long long)t * a.d8 + v) * 8;
-      Slots<HT>::fill(slot_h, pitch, h + at);
-      if (y) Slots<float>::fill(slot_y, pitch, y + at);
-    }
-    commit_copies();
-  };
-  const int step = gridDim.x * groups;
-  int t = blockIdx.x * groups + group;
-  ahead(t);
-  float wp[8], wn[8];
-  load_weight(w_post, v, in, a.w_offset, wp);
-  load_weight(w_next, v, in, a.w_offset, wn);
-  for (; t < a.T; t += step) {
-    const long long at = ((long long)t * a.d8 + v) * 8;
-    float scale = a.out_scale;
-    if (gate) scale *= gate[t];
-    float hv[8], yv[8];
-    wait_copies<0>();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) hv[j] = yv[j] = 0.f;
-    if (in) {
-      Slots<HT>::read(slot_h, pitch, hv);
-      if (y) Slots<float>::read(slot_y, pitch, yv);
-    }
-    ahead(t + step);
-    if (y) {
-      if (w_post) {
-        float s = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s = fmaf(yv[j], yv[j], s);
-        s = group_sum(s, a.W, group, warp, lane, red);
-        scale *= rsqrtf(fmaf(s, a.inv_d, a.eps));
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) hv[j] = fmaf(yv[j] * wp[j], scale, hv[j] * a.res_scale);
-      if (in) store8_if(a.whole, h_out + at, hv);
-    }
-    if (w_next) {
-      float s = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s = fmaf(hv[j], hv[j], s);
-      s = group_sum(s, a.W, group, warp, lane, red + 32);
-      const float r = rsqrtf(fmaf(s, a.inv_d, a.eps));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) hv[j] *= r * wn[j];
-      if (in) store8(x + at, hv);
-    }
-  }
-}
-
-// 8 elements of the stream as they are stored, so that a bf16 row takes half the registers
-// while it waits for the row's sums.
-template <class T>
-struct Held;
-template <>
-struct Held<float> {
-  float v[8];
-  __device__ void read(uint32_t slot, uint32_t pitch) { Slots<float>::read(slot, pitch, v); }
-  __device__ float operator[](int j) const { return v[j]; }
-};
-template <>
-struct Held<__nv_bfloat16> {
-  uint32_t w[4];
-  __device__ void read(uint32_t slot, uint32_t pitch) {
-    const uint4 a = slot16(slot);
-    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-  }
-  __device__ float operator[](int j) const {
-    return __uint_as_float(j % 2 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
-  }
-};
-
-__device__ __forceinline__ void read4(uint32_t slot, float* v) {
-  const uint4 a = slot16(slot);
-  v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y);
-  v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
 }
 
 // The six sums of a row over its group of W warps, on every thread.  `red`: 8 * 17 floats.
@@ -200,58 +151,147 @@ __device__ __forceinline__ void group_sum8(float (&v)[8], int W, int group, int 
   for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(0xffffffffu, s, 4 * i);
 }
 
-constexpr int kBwdV = 2;                        // 8-column steps of a thread
-constexpr int kBwdThreads = 512;
-constexpr int kBwdRed = 2 * 8 * 17;             // floats of a group's two reduction buffers
-template <class HT>
-constexpr int bwd_units() {                     // 16-byte units of a thread: a row and weights
-  return kBwdV * (2 * Slots<HT>::kUnits + 4 + 4);
+// The next row's columns are copied to the thread's slots as soon as this row's are in
+// registers, so that memory works through both means of a row (two or three rows ahead gave
+// nothing: they only take L1 from the copies).
+template <class HT, class WT>
+__global__ void __launch_bounds__(1024)
+block_norm_kernel(const NormArgs a, const HT* h, const float* __restrict__ y,
+                  const float* __restrict__ gate, const WT* __restrict__ w_post,
+                  const WT* __restrict__ w_next, HT* h_out, __nv_bfloat16* __restrict__ x) {
+  constexpr int U = kFwdUnits;
+  extern __shared__ __align__(16) char smem[];
+  const int lane = threadIdx.x & 31;
+  const int group = (threadIdx.x >> 5) / a.W, warp = (threadIdx.x >> 5) % a.W;
+  const int groups = (blockDim.x >> 5) / a.W;
+  const Array<float> ys(smem_addr(smem), blockDim.x);
+  const Array<HT> hs(smem_addr(smem) + U * 16 * blockDim.x, blockDim.x);
+  float* red = reinterpret_cast<float*>(smem + U * (16 + Unit<HT>::kBytes) * blockDim.x) +
+               group * kFwdRed;
+  auto unit = [&](int i) { return (i * a.W + warp) * 32 + lane; };
+  auto ahead = [&](int t) {
+    if (t < a.T) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const long long at = ((long long)t * a.d4 + unit(i)) * 4;
+        if (unit(i) >= a.d4) continue;
+        Unit<HT>::copy(hs.slot(i), h + at);
+        if (y) Unit<float>::copy(ys.slot(i), y + at);
+      }
+    }
+    commit_copies();
+  };
+  const int step = gridDim.x * groups;
+  int t = blockIdx.x * groups + group;
+  ahead(t);
+  float wp[U][4], wn[U][4];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    load_weight(w_post, unit(i), unit(i) < a.d4, a.w_offset, wp[i]);
+    load_weight(w_next, unit(i), unit(i) < a.d4, a.w_offset, wn[i]);
+  }
+  for (; t < a.T; t += step) {
+    float scale = a.out_scale;
+    if (gate) scale *= gate[t];
+    Unit<HT> hu[U];
+    Unit<float> yu[U];
+    wait_copies<0>();
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      hu[i].read(hs.slot(i));
+      if (y) yu[i].read(ys.slot(i));
+    }
+    ahead(t + step);
+    float hv[U][4];
+    if (y) {
+      if (w_post) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (unit(i) < a.d4) s = fmaf(yu[i][j], yu[i][j], s);
+        s = group_sum(s, a.W, group, warp, lane, red);
+        scale *= rsqrtf(fmaf(s, a.inv_d, a.eps));
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          hv[i][j] = fmaf(yu[i][j] * wp[i][j], scale, hu[i][j] * a.res_scale);
+        if (unit(i) < a.d4) store4(h_out + ((long long)t * a.d4 + unit(i)) * 4, hv[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) hv[i][j] = hu[i][j];
+    }
+    if (w_next) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (unit(i) < a.d4) s = fmaf(hv[i][j], hv[i][j], s);
+      s = group_sum(s, a.W, group, warp, lane, red + kFwdRed / 2);
+      const float r = rsqrtf(fmaf(s, a.inv_d, a.eps));
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) hv[i][j] *= r * wn[i][j];
+        if (unit(i) < a.d4) store4(x + ((long long)t * a.d4 + unit(i)) * 4, hv[i]);
+      }
+    }
+  }
 }
 
-// A thread owns 16 columns of every row of its group.  The next row's columns are copied to
-// the thread's slots while this row is worked on (no thread reads another's slots).
+// Bytes of a thread's slots in the backward kernel: a row's units, then the weights'.
+template <class HT>
+constexpr int bwd_slot_bytes() {
+  return kBwdUnits * (2 * Unit<HT>::kBytes + 4 * 16);
+}
+
 template <class HT, class WT>
-__global__ void __launch_bounds__(kBwdThreads)
+__global__ void __launch_bounds__(kThreads)
 block_norm_backward_kernel(const NormArgs a, const HT* __restrict__ h_out,
                            const float* __restrict__ y, const float* __restrict__ gate,
                            const WT* __restrict__ w_post, const WT* __restrict__ w_next,
                            const HT* dh_out, const float* __restrict__ dx, HT* dh,
                            float* __restrict__ dy, float* __restrict__ dgate,
                            float* __restrict__ partial) {
-  constexpr int V = kBwdV, HU = Slots<HT>::kUnits;
+  constexpr int U = kBwdUnits;
   extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x & 31;
   const int group = (threadIdx.x >> 5) / a.W, warp = (threadIdx.x >> 5) % a.W;
   const int groups = (blockDim.x >> 5) / a.W;
-  const uint32_t pitch = blockDim.x * 16;
-  const uint32_t slots = smem_addr(smem) + threadIdx.x * 16;
-  float* red = reinterpret_cast<float*>(smem + bwd_units<HT>() * pitch) + group * kBwdRed;
-  // unit offsets: h', dh', y, dx, then the weights
-  auto slot = [&](int unit) { return slots + (uint32_t)unit * pitch; };
-  constexpr int kH = 0, kDh = V * HU, kY = 2 * V * HU, kDx = kY + 2 * V, kWp = kDx + 2 * V,
-                kWn = kWp + 2 * V;
-  bool in[V];
-  float gp[V][8], gn[V][8];
+  const uint32_t base = smem_addr(smem), step16 = U * 16 * blockDim.x;
+  const Array<float> ys(base, blockDim.x), qs(base + step16, blockDim.x);
+  const Array<float> wps(base + 2 * step16, blockDim.x), wns(base + 3 * step16, blockDim.x);
+  const uint32_t stream = base + 4 * step16;
+  const Array<HT> hs(stream, blockDim.x),
+      ds(stream + U * Unit<HT>::kBytes * blockDim.x, blockDim.x);
+  float* red = reinterpret_cast<float*>(smem + bwd_slot_bytes<HT>() * blockDim.x) + group * kBwdRed;
+  auto unit = [&](int i) { return (i * a.W + warp) * 32 + lane; };
   let_successor_start();  // it waits for this kernel's end; its launch need not
-  float4* own = reinterpret_cast<float4*>(smem) + threadIdx.x;
+  // what no copy fills stays zero: absent arrays, columns behind the row
 #pragma unroll
-  for (int i = 0; i < kWp; ++i) own[i * blockDim.x] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-  for (int u = 0; u < V; ++u) {
-    in[u] = (u * a.W + warp) * 32 + lane < a.d8;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) gp[u][j] = gn[u][j] = 0.f;
+  for (int i = 0; i < U; ++i) {
+    Unit<float>::clear(ys.slot(i));
+    Unit<float>::clear(qs.slot(i));
+    Unit<HT>::clear(hs.slot(i));
+    Unit<HT>::clear(ds.slot(i));
   }
   auto ahead = [&](int t) {
     if (t < a.T) {
 #pragma unroll
-      for (int u = 0; u < V; ++u) {
-        if (!in[u]) continue;
-        const long long at = ((long long)t * a.d8 + (u * a.W + warp) * 32 + lane) * 8;
-        if (w_next) Slots<HT>::fill(slot(kH + u * HU), pitch, h_out + at);
-        if (dh_out) Slots<HT>::fill(slot(kDh + u * HU), pitch, dh_out + at);
-        if (y) Slots<float>::fill(slot(kY + 2 * u), pitch, y + at);
-        if (w_next) Slots<float>::fill(slot(kDx + 2 * u), pitch, dx + at);
+      for (int i = 0; i < U; ++i) {
+        if (unit(i) >= a.d4) continue;
+        const long long at = ((long long)t * a.d4 + unit(i)) * 4;
+        if (w_next) Unit<HT>::copy(hs.slot(i), h_out + at);
+        if (dh_out) Unit<HT>::copy(ds.slot(i), dh_out + at);
+        if (y) Unit<float>::copy(ys.slot(i), y + at);
+        if (w_next) Unit<float>::copy(qs.slot(i), dx + at);
       }
     }
     commit_copies();
@@ -259,45 +299,45 @@ block_norm_backward_kernel(const NormArgs a, const HT* __restrict__ h_out,
   const int step = gridDim.x * groups;
   int t = blockIdx.x * groups + group, turn = 0;
   ahead(t);
+  float gp[U][4], gn[U][4];
 #pragma unroll
-  for (int u = 0; u < V; ++u) {
-    const int v = (u * a.W + warp) * 32 + lane;
-    float w[8];
-    load_weight(w_post, v, in[u], a.w_offset, w);
-    own[(kWp + 2 * u) * blockDim.x] = make_float4(w[0], w[1], w[2], w[3]);
-    own[(kWp + 2 * u + 1) * blockDim.x] = make_float4(w[4], w[5], w[6], w[7]);
-    load_weight(w_next, v, in[u], a.w_offset, w);
-    own[(kWn + 2 * u) * blockDim.x] = make_float4(w[0], w[1], w[2], w[3]);
-    own[(kWn + 2 * u + 1) * blockDim.x] = make_float4(w[4], w[5], w[6], w[7]);
+  for (int i = 0; i < U; ++i) {
+    float w[4];
+    load_weight(w_post, unit(i), unit(i) < a.d4, a.w_offset, w);
+    reinterpret_cast<float4*>(smem)[2 * U * blockDim.x + i * blockDim.x + threadIdx.x] =
+        make_float4(w[0], w[1], w[2], w[3]);
+    load_weight(w_next, unit(i), unit(i) < a.d4, a.w_offset, w);
+    reinterpret_cast<float4*>(smem)[3 * U * blockDim.x + i * blockDim.x + threadIdx.x] =
+        make_float4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) gp[i][j] = gn[i][j] = 0.f;
   }
   for (; t < a.T; t += step, turn ^= 1) {
-    Held<HT> hv[V], dv[V];
-    float yv[V][8], q[V][8];
+    Unit<HT> hu[U], du[U];
+    Unit<float> yu[U], qu[U];
     const float gt = gate ? gate[t] : 1.f;
     wait_copies<0>();
 #pragma unroll
-    for (int u = 0; u < V; ++u) {
-      hv[u].read(slot(kH + u * HU), pitch);
-      dv[u].read(slot(kDh + u * HU), pitch);
-      Slots<float>::read(slot(kY + 2 * u), pitch, yv[u]);
-      Slots<float>::read(slot(kDx + 2 * u), pitch, q[u]);
+    for (int i = 0; i < U; ++i) {
+      hu[i].read(hs.slot(i));
+      du[i].read(ds.slot(i));
+      yu[i].read(ys.slot(i));
+      qu[i].read(qs.slot(i));
     }
     ahead(t + step);
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 2 * V; ++i) {
-      float wp[4], wn[4];
-      read4(slot(kWp + i), wp);
-      read4(slot(kWn + i), wn);
+    for (int i = 0; i < U; ++i) {
+      Unit<float> wp, wn;
+      wp.read(wps.slot(i));
+      wn.read(wns.slot(i));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int u = i / 2, j = 4 * (i % 2) + k;
-        const float qw = q[u][j] * wn[k], yw = yv[u][j] * wp[k];
-        const float hj = hv[u][j];
+      for (int j = 0; j < 4; ++j) {
+        const float qw = qu[i][j] * wn[j], yw = yu[i][j] * wp[j], hj = hu[i][j];
         s[0] = fmaf(hj, hj, s[0]);
         s[1] = fmaf(qw, hj, s[1]);
-        s[2] = fmaf(yv[u][j], yv[u][j], s[2]);
-        s[3] = fmaf(dv[u][j], yw, s[3]);
+        s[2] = fmaf(yu[i][j], yu[i][j], s[2]);
+        s[3] = fmaf(du[i][j], yw, s[3]);
         s[4] = fmaf(qw, yw, s[4]);
         s[5] = fmaf(hj, yw, s[5]);
       }
@@ -314,27 +354,25 @@ block_norm_backward_kernel(const NormArgs a, const HT* __restrict__ h_out,
     const float back = w_post ? ry * ry * uy * a.inv_d : 0.f;
     const float res = y ? a.res_scale : 1.f;
     if (gate && warp == 0 && lane == 0) dgate[t] = a.out_scale * ry * uy;
-    float out[8];
 #pragma unroll
-    for (int i = 0; i < 2 * V; ++i) {
-      const int u = i / 2;
-      float wp[4], wn[4];
-      read4(slot(kWp + i), wp);
-      read4(slot(kWn + i), wn);
+    for (int i = 0; i < U; ++i) {
+      Unit<float> wp, wn;
+      wp.read(wps.slot(i));
+      wn.read(wns.slot(i));
+      float to_y[4], to_h[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int j = 4 * (i % 2) + k;
-        const float hj = hv[u][j], qa = q[u][j] * A;
-        gn[u][j] = fmaf(qa, hj, gn[u][j]);
-        const float g = fmaf(qa, wn[k], fmaf(-B, hj, dv[u][j]));
-        gp[u][j] = fmaf(g * scale, yv[u][j], gp[u][j]);
-        yv[u][j] = scale * fmaf(g, wp[k], -yv[u][j] * back);
-        out[j] = g * res;
+      for (int j = 0; j < 4; ++j) {
+        const float hj = hu[i][j], qa = qu[i][j] * A;
+        gn[i][j] = fmaf(qa, hj, gn[i][j]);
+        const float g = fmaf(qa, wn[j], fmaf(-B, hj, du[i][j]));
+        gp[i][j] = fmaf(g * scale, yu[i][j], gp[i][j]);
+        to_y[j] = scale * fmaf(g, wp[j], -yu[i][j] * back);
+        to_h[j] = g * res;
       }
-      if (i % 2 == 1 && in[u]) {
-        const long long at = ((long long)t * a.d8 + (u * a.W + warp) * 32 + lane) * 8;
-        if (y) store8_if(a.whole, dy + at, yv[u]);
-        store8_if(a.whole, dh + at, out);
+      if (unit(i) < a.d4) {
+        const long long at = ((long long)t * a.d4 + unit(i)) * 4;
+        if (y) store4(dy + at, to_y);
+        store4(dh + at, to_h);
       }
     }
   }
@@ -343,22 +381,21 @@ block_norm_backward_kernel(const NormArgs a, const HT* __restrict__ h_out,
   if (groups > 1) __syncthreads();
   for (int g = 0; g < groups; ++g) {
     if (group == g) {
-      float* out = g == groups - 1 ? partial + (long long)blockIdx.x * 2 * a.d8 * 8 : col;
+      float* out = g == groups - 1 ? partial + (long long)blockIdx.x * 2 * a.d4 * 4 : col;
 #pragma unroll
-      for (int u = 0; u < V; ++u) {
-        const int v = (u * a.W + warp) * 32 + lane;
-        if (!in[u]) continue;
+      for (int i = 0; i < U; ++i) {
+        if (unit(i) >= a.d4) continue;
         if (g > 0) {
-          float t8[8];
-          load8(col + v * 8, t8);
+          float t4[4];
+          load4(col + unit(i) * 4, t4);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) gp[u][j] += t8[j];
-          load8(col + (a.d8 + v) * 8, t8);
+          for (int j = 0; j < 4; ++j) gp[i][j] += t4[j];
+          load4(col + (a.d4 + unit(i)) * 4, t4);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) gn[u][j] += t8[j];
+          for (int j = 0; j < 4; ++j) gn[i][j] += t4[j];
         }
-        store8(out + v * 8, gp[u]);
-        store8(out + (a.d8 + v) * 8, gn[u]);
+        store4(out + unit(i) * 4, gp[i]);
+        store4(out + (a.d4 + unit(i)) * 4, gn[i]);
       }
     }
     if (groups > 1) __syncthreads();
@@ -393,11 +430,11 @@ norm_weight_grad_kernel(const float* __restrict__ partial, int rows, int d,
   }
 }
 
-NormArgs make_args(const moe_cfg& c, const moet_norm& n, int V) {
+NormArgs make_args(const moe_cfg& c, const moet_norm& n, int units) {
   NormArgs a;
   a.T = c.T;
-  a.d8 = c.d / 8;
-  a.W = (a.d8 + 32 * V - 1) / (32 * V);
+  a.d4 = c.d / 4;
+  a.W = (a.d4 + 32 * units - 1) / (32 * units);
   a.inv_d = 1.f / (float)c.d;
   a.eps = n.eps;
   a.w_offset = n.w_offset;
@@ -405,16 +442,10 @@ NormArgs make_args(const moe_cfg& c, const moet_norm& n, int V) {
   a.out_scale = n.out_scale;
   return a;
 }
-bool on_sectors(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (reinterpret_cast<uintptr_t>(p) & 31u) return false;
-  return true;
-}
 
-// Row groups of a CTA: as many as `threads` hold, but no more than it takes to give every SM
-// rows.
-int groups_of(int T, int W, int threads) {
-  const int fit = threads / 32 / W, sms = num_sms(), rows = (T + sms - 1) / sms;
+// Row groups of a CTA: as many as it holds, but no more than it takes to give every SM rows.
+int groups_of(int T, int W) {
+  const int fit = kThreads / 32 / W, sms = num_sms(), rows = (T + sms - 1) / sms;
   const int n = fit < rows ? fit : rows;
   return n < 1 ? 1 : n;
 }
@@ -423,19 +454,18 @@ template <class HT, class WT>
 cudaError_t forward(const moe_cfg& c, const moet_norm& n, const void* h, const float* y,
                     const float* gate, const void* wp, const void* wn, void* h_out,
                     uint16_t* x, cudaStream_t st) {
-  constexpr int kUnits = Slots<HT>::kUnits + 2;
-  NormArgs a = make_args(c, n, 1);
-  a.whole = on_sectors({h_out});
-  const int groups = groups_of(c.T, a.W, kFwdThreads), threads = groups * a.W * 32;
+  constexpr int kSlots = kFwdUnits * (16 + Unit<HT>::kBytes);  // bytes a thread
+  const NormArgs a = make_args(c, n, kFwdUnits);
+  const int groups = groups_of(c.T, a.W), threads = groups * a.W * 32;
   auto kernel = block_norm_kernel<HT, WT>;
   static OncePerDevice once;
   const cudaError_t err = once_per_device(once, [&](int&) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kUnits * 1024 * 16 + 16 * 64 * 4);
+                                kSlots * 1024 + 16 * kFwdRed * 4);
   });
   if (err != cudaSuccess) return err;
   const int want = (c.T + groups - 1) / groups, cap = num_sms() * (1024 / threads);
-  kernel<<<want < cap ? want : cap, threads, kUnits * threads * 16 + groups * 64 * 4, st>>>(
+  kernel<<<want < cap ? want : cap, threads, kSlots * threads + groups * kFwdRed * 4, st>>>(
       a, static_cast<const HT*>(h), y, gate, static_cast<const WT*>(wp),
       static_cast<const WT*>(wn), static_cast<HT*>(h_out),
       reinterpret_cast<__nv_bfloat16*>(x));
@@ -447,20 +477,18 @@ cudaError_t backward(const moe_cfg& c, const moet_norm& n, const void* h_out, co
                      const float* gate, const void* wp, const void* wn, const void* dh_out,
                      const float* dx, void* dh, float* dy, float* dgate, float* dw_post,
                      float* dw_next, void* ws, cudaStream_t st) {
-  NormArgs a = make_args(c, n, kBwdV);
-  a.whole = on_sectors({dh, dy});
-  const int sms = num_sms();
-  const int groups = groups_of(c.T, a.W, kBwdThreads), threads = groups * a.W * 32;
-  const size_t smem = (size_t)bwd_units<HT>() * threads * 16 + (size_t)groups * kBwdRed * 4;
+  const NormArgs a = make_args(c, n, kBwdUnits);
+  const int sms = num_sms(), groups = groups_of(c.T, a.W), threads = groups * a.W * 32;
+  const size_t smem = (size_t)bwd_slot_bytes<HT>() * threads + (size_t)groups * kBwdRed * 4;
   auto kernel = block_norm_backward_kernel<HT, WT>;
   static OncePerDevice once;
   cudaError_t err = once_per_device(once, [&](int&) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                bwd_units<HT>() * kBwdThreads * 16 + 16 * kBwdRed * 4);
+                                bwd_slot_bytes<HT>() * kThreads + kThreads / 32 * kBwdRed * 4);
   });
   if (err != cudaSuccess) return err;
   int grid = (c.T + groups - 1) / groups;
-  const int cap = sms * (kBwdThreads / threads);
+  const int cap = sms * (kThreads / threads);
   if (grid > cap) grid = cap;
   if (grid > kMaxPartials) grid = kMaxPartials;
   if (grid > 0) {

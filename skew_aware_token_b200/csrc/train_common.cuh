@@ -52,37 +52,10 @@ __device__ __forceinline__ void bf16x8_to_f32(const uint4 a, float* v) {
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
-  bf16x8_to_f32(*reinterpret_cast<const uint4*>(p), v);
-}
-__device__ __forceinline__ void store8(float* p, const float* v) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-// With 32-byte alignment a lane's 8 values leave in one store of a whole sector; in two, each
-// store of the warp touches every sector and fills half of it.
-__device__ __forceinline__ void store8_whole(float* p, const float* v) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
-               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
-}
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&t);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* v) {
-  *reinterpret_cast<uint4*>(p) =
-      make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                 pack_bf16x2(v[6], v[7]));
-}
-
-__device__ __forceinline__ void store8_whole(__nv_bfloat16* p, const float* v) { store8(p, v); }
-template <class T>
-__device__ __forceinline__ void store8_if(bool whole, T* p, const float* v) {
-  if (whole) store8_whole(p, v);
-  else store8(p, v);
-}
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
