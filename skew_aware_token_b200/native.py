@@ -270,6 +270,36 @@ _SIGNATURES.update({
 })
 
 
+LISTS_LIB_PATH = os.path.join(os.path.dirname(LIB_PATH), "libmoeskew_lists.so")
+_lists = None
+
+
+def read_gradients(grads, sizes, device: int, tensors) -> None:
+    """Checks a list or tuple of gradients (fp32 or bf16, contiguous, sizes[i] elements, on
+    CUDA device `device`) and fills in their addresses and types in the MoetAdamwTensor array
+    `tensors`.  `sizes`: a ctypes array of int64."""
+    global _lists
+    if _lists is None:
+        if not os.path.exists(LISTS_LIB_PATH):
+            raise RuntimeError(f"{LISTS_LIB_PATH} is missing: build it with "
+                               "`python -m skew_aware_token_b200.build`")
+        handle = ctypes.PyDLL(LISTS_LIB_PATH)  # the interpreter's lock stays held
+        fn = handle.moet_read_gradients
+        fn.restype = ctypes.c_int64
+        fn.argtypes = [ctypes.py_object, ctypes.c_int64, ctypes.c_int32, _VP, _VP]
+        _lists = fn
+    rc = _lists(grads, len(sizes), device, sizes, tensors)
+    if rc:
+        i, what = divmod(rc, 8)
+        if what == 1:
+            raise ValueError(f"a list of {len(sizes)} gradients is needed")
+        if what == 2:
+            raise TypeError(f"grads[{i}] must be a torch.float32 or torch.bfloat16 tensor")
+        if what == 3:
+            raise TypeError(f"grads[{i}] must be on cuda:{device}")
+        raise ValueError(f"grads[{i}] must be contiguous with {sizes[i]} elements")
+
+
 def call(fn: str, *args) -> None:
     """Entry point `fn` on addresses that its caller has checked (ctypes structures by
     reference, the stream's handle last); raises as the wrappers do."""

@@ -21,20 +21,15 @@ its outputs are views that the next call overwrites.
 """
 from __future__ import annotations
 
-import array
 import collections
 import ctypes
-import operator
 
-import numpy as np
 import torch
 
 from . import native as N
 
 _TYPES = {torch.float32: N.MOET_F32, torch.bfloat16: N.MOET_BF16,
           torch.float8_e4m3fn: N.MOET_E4M3}
-_GRAD_TYPES = {torch.float32, torch.bfloat16}
-_dtype_of = operator.attrgetter("dtype")
 
 
 def _device(device) -> torch.device:
@@ -373,15 +368,7 @@ class AdamW(_OnDevice):
         for (_, end, a), (begin, _, b) in zip(spans, spans[1:]):
             if begin < end:
                 raise ValueError(f"{a} and {b} share memory")
-        self._sizes = sizes
-        # the descriptors' fields that a step fills in, as arrays over the tensors
-        at = {n: getattr(N.MoetAdamwTensor, n).offset for n in ("g", "g_dtype")}
-        fields = np.frombuffer(self._tensors, dtype=np.dtype(
-            {"names": list(at), "formats": [np.uint64, np.int32], "offsets": list(at.values()),
-             "itemsize": ctypes.sizeof(N.MoetAdamwTensor)}))
-        self._g, self._g_dtype = fields["g"], fields["g_dtype"]
-        self._devices = [dev.index] * count
-        self._types = None  # of the last step's gradients, as the descriptors hold them
+        self._sizes = (ctypes.c_int64 * count)(*sizes)
         self._opt = N.MoetAdamw(float(betas[0]), float(betas[1]), float(eps))
         self.lr = torch.full((4,), float(lr), device=dev)
         self.steps = torch.tensor([step, 0, 0, 0], dtype=torch.int32, device=dev)
@@ -394,27 +381,9 @@ class AdamW(_OnDevice):
         """One step with `grads` (fp32 or bf16, one a parameter, of its size).  `grad_scale`:
         fp32 device tensor that multiplies them (a clip or a loss scale's inverse); when it
         is not finite, the step is left out."""
-        grads = list(grads)
-        if len(grads) != len(self.params):
-            raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
-        # over all of them at once: a loop over hundreds of tensors costs more than the step
-        try:
-            types = list(map(_dtype_of, grads))
-            devices = list(map(torch.Tensor.get_device, grads))
-        except (AttributeError, TypeError):
-            raise TypeError("grads must be tensors") from None
-        if devices != self._devices:
-            raise TypeError(f"grads must be on {self.device}")
-        if types != self._types:
-            if not _GRAD_TYPES.issuperset(types):
-                raise TypeError("grads must be torch.float32 or torch.bfloat16 tensors")
-            self._g_dtype[:] = list(map(_TYPES.__getitem__, types))
-            self._types = types
-        if list(map(torch.Tensor.numel, grads)) != self._sizes or \
-                not all(map(torch.Tensor.is_contiguous, grads)):
-            raise ValueError("grads must be contiguous and of their parameters' sizes")
-        self._g[:] = array.array("Q", map(torch.Tensor.data_ptr, grads))
+        grads = grads if isinstance(grads, (list, tuple)) else list(grads)
+        N.read_gradients(grads, self._sizes, self._index, self._tensors)
         scale = _need(grad_scale, "grad_scale", torch.float32, 1, self._index, True)
         self._call("moet_adamw_step",
-                   (self._tensors, len(grads), ctypes.byref(self._opt), self.lr.data_ptr(),
+                   (self._tensors, len(self._sizes), ctypes.byref(self._opt), self.lr.data_ptr(),
                     scale, self.steps.data_ptr()), stream)

@@ -205,6 +205,24 @@ def test_classes_refuse_the_cpu():
         train.BlockNorm(wl, h_dtype=torch.float16)
 
 
+def test_gradient_lists_are_checked():
+    """The native reader of gradient lists refuses what is not a list of the right tensors and
+    says which one it is."""
+    sizes, t = (ctypes.c_int64 * 3)(5, 5, 5), (N.MoetAdamwTensor * 3)()
+    host = [torch.zeros(5) for _ in range(3)]
+    for bad, error, text in (
+            (host, TypeError, r"grads\[0\] must be on cuda:0"),
+            ([1, 2, 3], TypeError, r"grads\[0\] must be a torch"), (host[:2], ValueError, "list of 3"),
+            ((None,) * 3, TypeError, r"grads\[0\]"), (torch.zeros(3), ValueError, "list of 3"),
+            ([torch.zeros(5, dtype=torch.int32)] * 3, TypeError, r"grads\[0\] must be a torch"),
+            ([torch.zeros(5, dtype=torch.float64)] * 3, TypeError, r"grads\[0\]"),
+            ([torch.zeros(5, device="meta")] * 3, TypeError, r"grads\[0\] must be on"),
+            ([torch.zeros(5).to_sparse()] * 3, TypeError, r"grads\[0\] must be on")):
+        with pytest.raises(error, match=text):
+            N.read_gradients(bad, sizes, 0, t)
+    assert all(not e.g for e in t)
+
+
 # ---- the 64-bit forms, against differences ----
 def _g(seed):
     g = torch.Generator()
