@@ -1,5 +1,5 @@
 """Builds libmoeskew.so in-tree with nvcc for sm_100a (no GPU needed to build), and beside it
-libmoeskew_lists.so, the host code that reads lists of torch tensors (g++, torch's headers).
+libmoeskew_args.so, the host code that reads torch tensors (g++, torch's headers).
 
     python -m skew_aware_token_b200.build [--force]
 """
@@ -20,8 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoeskew.so")
-LISTS_LIB = os.path.join(PKG, "libmoeskew_lists.so")
-LISTS_SOURCE = os.path.join(CSRC, "tensor_list.cpp")
+ARGS_LIB = os.path.join(PKG, "libmoeskew_args.so")
+ARGS_SOURCE = os.path.join(CSRC, "torch_args.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -48,33 +48,33 @@ def _deps() -> list[str]:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not _lists_up_to_date():
+    if not os.path.exists(LIB) or not _args_up_to_date():
         return False
     t = os.path.getmtime(LIB)
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
-def _lists_up_to_date() -> bool:
-    return os.path.exists(LISTS_LIB) and all(
-        os.path.getmtime(p) <= os.path.getmtime(LISTS_LIB)
-        for p in [LISTS_SOURCE] + glob.glob(os.path.join(INCLUDE, "*.h")))
+def _args_up_to_date() -> bool:
+    return os.path.exists(ARGS_LIB) and all(
+        os.path.getmtime(p) <= os.path.getmtime(ARGS_LIB)
+        for p in [ARGS_SOURCE] + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
-def _build_lists() -> None:
-    """libmoeskew_lists.so: linked to the torch that this interpreter imports."""
+def _build_args() -> None:
+    """libmoeskew_args.so: linked to the torch that this interpreter imports."""
     torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
     include = os.path.join(torch_dir, "include")
     lib = os.path.join(torch_dir, "lib")
-    tmp = LISTS_LIB + ".tmp"
+    tmp = ARGS_LIB + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            "-fvisibility=hidden", "-I", INCLUDE, "-I", include, "-I",
            os.path.join(include, "torch", "csrc", "api", "include"), "-I",
-           sysconfig.get_paths()["include"], LISTS_SOURCE, "-o", tmp, "-L", lib,
+           sysconfig.get_paths()["include"], ARGS_SOURCE, "-o", tmp, "-L", lib,
            "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on {LISTS_SOURCE}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LISTS_LIB)
+        raise RuntimeError(f"g++ failed on {ARGS_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, ARGS_LIB)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -97,10 +97,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        lists = ex.submit(_build_lists) if force or not _lists_up_to_date() else None
+        args = ex.submit(_build_args) if force or not _args_up_to_date() else None
         objs = list(ex.map(compile_one, _sources()))
-        if lists:
-            lists.result()
+        if args:
+            args.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

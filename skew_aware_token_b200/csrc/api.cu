@@ -8,10 +8,15 @@
 namespace moe {
 
 int num_sms() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
-  return n > 0 ? n : 1;
+  static OncePerDevice once;
+  int n = 0;
+  const cudaError_t err = once_per_device(once, [](int& v) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e != cudaSuccess ? e
+                            : cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+  }, &n);
+  return err == cudaSuccess && n > 0 ? n : 1;
 }
 
 // Checks shared by every stage.

@@ -270,25 +270,67 @@ _SIGNATURES.update({
 })
 
 
-LISTS_LIB_PATH = os.path.join(os.path.dirname(LIB_PATH), "libmoeskew_lists.so")
-_lists = None
+# ---- torch tensors read natively (csrc/torch_args.cpp) ----
+ARGS_LIB_PATH = os.path.join(os.path.dirname(LIB_PATH), "libmoeskew_args.so")
+_ARG_TYPES = {torch.float32: MOET_F32, torch.bfloat16: MOET_BF16,
+              torch.float8_e4m3fn: MOET_E4M3, torch.int32: 3, torch.uint8: 4}
+
+
+class _Arg(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("optional", ctypes.c_int32), ("n", ctypes.c_int64)]
+
+
+_args_lib = None
+
+
+def _args() -> ctypes.PyDLL:
+    global _args_lib
+    if _args_lib is None:
+        if not os.path.exists(ARGS_LIB_PATH):
+            raise RuntimeError(f"{ARGS_LIB_PATH} is missing: build it with "
+                               "`python -m skew_aware_token_b200.build`")
+        handle = ctypes.PyDLL(ARGS_LIB_PATH)  # the interpreter's lock stays held
+        for fn in (handle.moet_read_arguments, handle.moet_read_gradients):
+            fn.restype = ctypes.c_int64
+            fn.argtypes = [ctypes.py_object, ctypes.c_int64, ctypes.c_int32, _VP, _VP]
+        _args_lib = handle
+    return _args_lib
+
+
+class Arguments:
+    """The tensors that a call takes: (name, dtype, elements, optional) of each.  read() checks
+    a tuple of them and returns their addresses (None for one left out): contiguous tensors of
+    that dtype on CUDA device `device` with that many elements, or flat buffers of at least as
+    many."""
+
+    def __init__(self, device: int, *specs):
+        self.device, self.specs = device, specs
+        self._c = (_Arg * len(specs))(*[_Arg(_ARG_TYPES[dt], bool(opt), n)
+                                        for _, dt, n, opt in specs])
+        self._read, self._out = _args().moet_read_arguments, _VP * len(specs)
+        self._n = len(specs)
+
+    def read(self, *tensors):
+        out = self._out()  # this call's: two threads may use one object
+        rc = self._read(tensors, self._n, self.device, self._c, out)
+        if rc:
+            i, what = divmod(rc, 8)
+            name, dtype, n, _ = self.specs[i]
+            if what == 5:
+                raise TypeError(f"{name} is needed")
+            if what == 3:
+                raise TypeError(f"{name} must be a tensor on cuda:{self.device}")
+            if what == 2:
+                raise TypeError(f"{name} must be {dtype}, not {tensors[i].dtype}")
+            raise ValueError(f"{name} must be contiguous with {n} elements")
+        return out
 
 
 def read_gradients(grads, sizes, device: int, tensors) -> None:
     """Checks a list or tuple of gradients (fp32 or bf16, contiguous, sizes[i] elements, on
     CUDA device `device`) and fills in their addresses and types in the MoetAdamwTensor array
     `tensors`.  `sizes`: a ctypes array of int64."""
-    global _lists
-    if _lists is None:
-        if not os.path.exists(LISTS_LIB_PATH):
-            raise RuntimeError(f"{LISTS_LIB_PATH} is missing: build it with "
-                               "`python -m skew_aware_token_b200.build`")
-        handle = ctypes.PyDLL(LISTS_LIB_PATH)  # the interpreter's lock stays held
-        fn = handle.moet_read_gradients
-        fn.restype = ctypes.c_int64
-        fn.argtypes = [ctypes.py_object, ctypes.c_int64, ctypes.c_int32, _VP, _VP]
-        _lists = fn
-    rc = _lists(grads, len(sizes), device, sizes, tensors)
+    rc = _args().moet_read_gradients(grads, len(sizes), device, sizes, tensors)
     if rc:
         i, what = divmod(rc, 8)
         if what == 1:

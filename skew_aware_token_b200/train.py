@@ -39,27 +39,6 @@ def _device(device) -> torch.device:
     return torch.device("cuda", torch.cuda.current_device()) if dev.index is None else dev
 
 
-def _need(t, name, dtype, n, index, optional=False):
-    """The address of one array argument, after its checks: a contiguous tensor of `dtype` on
-    CUDA device `index` with `n` elements, or a flat buffer of at least that many (what
-    MoeLayer owns).  None when it is left out."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n and \
-            t.get_device() == index and t.is_contiguous():
-        return t.data_ptr()
-    if t is None:
-        if optional:
-            return None
-        raise TypeError(f"{name} is needed")
-    # what is wrong with it, or a flat buffer
-    if not isinstance(t, torch.Tensor) or t.get_device() != index:
-        raise TypeError(f"{name} must be a tensor on cuda:{index}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if not t.is_contiguous() or t.numel() < n or t.dim() != 1:
-        raise ValueError(f"{name} must be contiguous with {n} elements")
-    return t.data_ptr()
-
-
 # The current device and its current stream's handle without the objects around them (a fifth
 # of a small call's time).
 _device_index = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -116,7 +95,18 @@ class RouterLoss(_OnDevice):
         self.dlogits = self._dlogits[:T * E].view(T, E)
         self.workspace = z(size, dt=torch.uint8)
         self.status = z(4, dt=torch.int32)
-        self._rows = N.moe_workspace_size(self.cfg, N.MOE_WS_ROWS)
+        f32, i32, rows = torch.float32, torch.int32, N.moe_workspace_size(self.cfg, N.MOE_WS_ROWS)
+        batch = (("token_mask", torch.uint8, T, True), ("seq_off", i32, S + 1, S == 1))
+        x, ids = ("logits", f32, T * E, False), ("topk_ids", i32, T * k, False)
+        through_gates = (ids, ("topk_gates", f32, T * k, False), ("dy", f32, T * self.cfg.d, False),
+                         ("o", torch.bfloat16, rows * self.cfg.d, False),
+                         ("tok_row", i32, T * k, False))
+        through_losses = (("dloss", f32, 2, False), x, *batch)
+        index = self._index
+        self._loss_args = N.Arguments(index, x, ids, *batch)
+        self._gate_args = N.Arguments(index, *through_gates)
+        self._dloss_args = N.Arguments(index, *through_losses)
+        self._both_args = N.Arguments(index, *through_gates, *through_losses)
         # the addresses of the buffers above, in the entry points' order
         self._outputs = [t.data_ptr() for t in (self.losses, self.counts, self.probs,
                                                 self.seq_info, self._lse, self.workspace,
@@ -124,23 +114,12 @@ class RouterLoss(_OnDevice):
         self._saved = [t.data_ptr() for t in (self.counts, self.seq_info, self._lse)]
         self._grads = [t.data_ptr() for t in (self._dgates, self._dlogits, self.status)]
 
-    def _batch(self, token_mask, seq_off):
-        mask = off = None
-        if token_mask is not None:
-            mask = _need(token_mask, "token_mask", torch.uint8, self.cfg.T, self._index)
-        if seq_off is not None or self.n_seq != 1:
-            off = _need(seq_off, "seq_off", torch.int32, self.n_seq + 1, self._index)
-        return mask, off
-
     def __call__(self, logits, topk_ids, token_mask=None, seq_off=None, stream=None):
         """fp32 [2]: balance loss and z loss of logits fp32 [T, E] and the router's topk_ids
         int32 [T, k].  token_mask uint8 [T] leaves tokens out; seq_off int32 [n_seq + 1] are
         the sequences' bounds (None with one sequence: the whole batch)."""
-        c, dev = self.cfg, self._index
-        x = _need(logits, "logits", torch.float32, c.T * c.E, dev)
-        ids = _need(topk_ids, "topk_ids", torch.int32, c.T * c.k, dev)
-        mask, off = self._batch(token_mask, seq_off)
-        if c.T == 0:  # empty tensors have no address
+        x, ids, mask, off = self._loss_args.read(logits, topk_ids, token_mask, seq_off)
+        if self.cfg.T == 0:  # empty tensors have no address
             x, ids, mask = self._grads[1], self._grads[1], None
         self._call("moet_balance_loss",
                    (self._cfg, x, ids, mask, off, self.n_seq, *self._outputs), stream)
@@ -152,22 +131,18 @@ class RouterLoss(_OnDevice):
         the forward call on the same logits, ids, mask and sequences), the gates' part with
         dy (fp32 [T, d]), o (the expert output rows, bf16 [R_max, d]) and tok_row, or both.
         The gates' gradient is in `dgates` then."""
-        c, dev = self.cfg, self._index
         gates = dy is not None or o is not None or tok_row is not None
-        if not gates and dloss is None:
+        ids = g = dy_p = o_p = row = dl = x = mask = off = None
+        if gates and dloss is not None:
+            ids, g, dy_p, o_p, row, dl, x, mask, off = self._both_args.read(
+                topk_ids, topk_gates, dy, o, tok_row, dloss, logits, token_mask, seq_off)
+        elif gates:
+            ids, g, dy_p, o_p, row = self._gate_args.read(topk_ids, topk_gates, dy, o, tok_row)
+        elif dloss is not None:
+            dl, x, mask, off = self._dloss_args.read(dloss, logits, token_mask, seq_off)
+        else:
             raise ValueError("nothing to take the gradient of: give dloss, or dy, o and tok_row")
-        x = ids = g = dy_p = o_p = row = mask = off = dl = None
-        if gates:
-            ids = _need(topk_ids, "topk_ids", torch.int32, c.T * c.k, dev)
-            g = _need(topk_gates, "topk_gates", torch.float32, c.T * c.k, dev)
-            dy_p = _need(dy, "dy", torch.float32, c.T * c.d, dev)
-            o_p = _need(o, "o", torch.bfloat16, self._rows * c.d, dev)
-            row = _need(tok_row, "tok_row", torch.int32, c.T * c.k, dev)
-        if dloss is not None:
-            dl = _need(dloss, "dloss", torch.float32, 2, dev)
-            x = _need(logits, "logits", torch.float32, c.T * c.E, dev)
-            mask, off = self._batch(token_mask, seq_off)
-        if c.T == 0:
+        if self.cfg.T == 0:
             return self.dlogits
         dgates, dlogits, status = self._grads
         self._call("moet_router_backward",
@@ -221,36 +196,30 @@ class BlockNorm(_OnDevice):
             self.dw_post, self.dw_next = new(torch.float32, d), new(torch.float32, d)
             self.workspace = new(torch.uint8, size)
         self._refs = (ctypes.byref(self.cfg), ctypes.byref(self.norm))
-
-    def _inputs(self, h, y, gate, w_post, w_next):
-        T, d, dev = self.cfg.T, self.cfg.d, self._index
-        if y is None and (gate is not None or w_post is not None):
-            raise ValueError("gate and w_post belong to y")
-        return (_need(h, "h", self.h_dtype, T * d, dev),
-                _need(y, "y", torch.float32, T * d, dev, True),
-                None if gate is None else _need(gate, "gate", torch.float32, T, dev),
-                _need(w_post, "w_post", self.w_dtype, d, dev, True),
-                _need(w_next, "w_next", self.w_dtype, d, dev, True))
+        f32, rows = torch.float32, T * d
+        inputs = (("h", h_dtype, rows, False), ("y", f32, rows, True), ("gate", f32, T, True),
+                  ("w_post", w_dtype, d, True), ("w_next", w_dtype, d, True))
+        self._args = N.Arguments(self._index, *inputs, ("h_out", h_dtype, rows, True))
+        self._grad_args = N.Arguments(self._index, *inputs, ("dh_out", h_dtype, rows, True),
+                                      ("dx", f32, rows, True))
+        self._x = self.x.data_ptr()
 
     def __call__(self, h, y=None, gate=None, w_post=None, w_next=None, h_out=None, stream=None):
         """(h_out, x): the residual stream behind the block and, with w_next, the next
         block's bf16 rows.  Without y, h_out is h itself (a norm before the first block).
         `h_out=` takes the result's place in the caller's buffer; it may be h itself."""
-        c = self.cfg
-        inputs = self._inputs(h, y, gate, w_post, w_next)
-        if y is None and w_next is None:
-            raise ValueError("nothing to compute: give y, w_next or both")
         if y is None:
-            if h_out is not None:
-                raise ValueError("h_out is written only with y")
-            to = None
-        else:
-            h_out = self.h_out if h_out is None else h_out
-            to = _need(h_out, "h_out", self.h_dtype, c.T * c.d, self._index)
+            if w_next is None:
+                raise ValueError("nothing to compute: give y, w_next or both")
+            if gate is not None or w_post is not None or h_out is not None:
+                raise ValueError("gate, w_post and h_out belong to y")
+        elif h_out is None:
+            h_out = self.h_out
+        inputs = self._args.read(h, y, gate, w_post, w_next, h_out)
         x = None if w_next is None else self.x
-        if c.T:
-            self._call("moet_block_norm", (*self._refs, *inputs, to,
-                                           None if x is None else x.data_ptr()), stream)
+        if self.cfg.T:
+            self._call("moet_block_norm",
+                       (*self._refs, *inputs, None if x is None else self._x), stream)
         return (h if y is None else h_out), x
 
     def backward(self, h_out, y=None, gate=None, w_post=None, w_next=None, dh_out=None, dx=None,
@@ -260,21 +229,19 @@ class BlockNorm(_OnDevice):
         an argument that is None are None."""
         if not self.train:
             raise ValueError("built without train=True")
-        c = self.cfg
-        T, d, dev = c.T, c.d, self._index
-        inputs = self._inputs(h_out, y, gate, w_post, w_next)
-        into = (_need(dh_out, "dh_out", self.h_dtype, T * d, dev, True),
-                _need(dx, "dx", torch.float32, T * d, dev, True))
+        if y is None and (gate is not None or w_post is not None):
+            raise ValueError("gate and w_post belong to y")
         if (w_next is None) != (dx is None):
             raise ValueError("dx and w_next are given together")
         if dh_out is None and dx is None:
             raise ValueError("give dh_out, dx or both")
+        inputs = self._grad_args.read(h_out, y, gate, w_post, w_next, dh_out, dx)
         only = lambda buf, arg: None if arg is None else buf
         g = BlockNormGrads(self.dh, only(self.dy, y), only(self.dgate, gate),
                            only(self.dw_post, w_post), only(self.dw_next, w_next))
-        if T:
+        if self.cfg.T:
             self._call("moet_block_norm_backward",
-                       (*self._refs, *inputs, *into,
+                       (*self._refs, *inputs,
                         *[None if t is None else t.data_ptr() for t in g],
                         self.workspace.data_ptr()), stream)
         else:
@@ -341,7 +308,6 @@ class AdamW(_OnDevice):
         for i, p in enumerate(self.params):
             if p.dtype not in (torch.float32, torch.bfloat16):
                 raise TypeError("params must be torch.float32 or torch.bfloat16")
-            _need(p, f"params[{i}]", p.dtype, sizes[i], dev.index)
             own = [("m", self.m[i], state, sizes[i]), ("v", self.v[i], state, sizes[i])]
             if state_bits == 8:
                 own += [("m_scale", self.m_scale[i], torch.float32, blocks[i]),
@@ -351,9 +317,10 @@ class AdamW(_OnDevice):
                 if p.dtype is not torch.bfloat16:
                     raise ValueError("fp32 weights have no master")
                 own.append(("master", w, torch.float32, sizes[i]))
+            own.append(("params", p, p.dtype, sizes[i]))
+            N.Arguments(dev.index, *[(f"{name}[{i}]", dt, n, False) for name, _, dt, n in own]
+                        ).read(*[t for _, t, _, _ in own])
             for name, t, dt, n in own:
-                _need(t, f"{name}[{i}]", dt, n, dev.index)
-            for name, t, dt, n in own + [("params", p, p.dtype, sizes[i])]:
                 if n:
                     spans.append((t.data_ptr(), t.data_ptr() + n * t.element_size(),
                                   f"{name}[{i}]"))
@@ -369,6 +336,7 @@ class AdamW(_OnDevice):
             if begin < end:
                 raise ValueError(f"{a} and {b} share memory")
         self._sizes = (ctypes.c_int64 * count)(*sizes)
+        self._scale_args = N.Arguments(dev.index, ("grad_scale", torch.float32, 1, False))
         self._opt = N.MoetAdamw(float(betas[0]), float(betas[1]), float(eps))
         self.lr = torch.full((4,), float(lr), device=dev)
         self.steps = torch.tensor([step, 0, 0, 0], dtype=torch.int32, device=dev)
@@ -383,7 +351,7 @@ class AdamW(_OnDevice):
         is not finite, the step is left out."""
         grads = grads if isinstance(grads, (list, tuple)) else list(grads)
         N.read_gradients(grads, self._sizes, self._index, self._tensors)
-        scale = _need(grad_scale, "grad_scale", torch.float32, 1, self._index, True)
+        scale = None if grad_scale is None else self._scale_args.read(grad_scale)[0]
         self._call("moet_adamw_step",
                    (self._tensors, len(self._sizes), ctypes.byref(self._opt), self.lr.data_ptr(),
                     scale, self.steps.data_ptr()), stream)
