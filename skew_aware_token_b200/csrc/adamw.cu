@@ -18,11 +18,11 @@
 //
 // Bound by HBM: fp32 states 200 us for 50 M fp32 weights with bf16 gradients (26 bytes each,
 // 6.5 TB/s, a copy's rate).  With bf16 weights, fp32 gradients and 8-bit states 12 bytes an
-// element carry 46 instructions: 402 M weights take 850 us at first and 925 us once the power
-// limit has lowered the clocks (4.86 GB: 741 us at a copy's rate).  The same accesses without
-// the arithmetic take 810 to 830 us, so what is left above them is the arithmetic that they
-// do not hide; streaming stores, wider or narrower CTAs and two or four blocks a warp gave
-// nothing or cost time.
+// element carry 46 instructions: 402 M weights take 875 us at the clocks that the power limit
+// leaves (4.86 GB: 741 us at a copy's rate).  The same accesses without the arithmetic take
+// 810 to 830 us; the two blocks copied ahead hide most of it (one ahead: 942 us, none: 960).
+// Streaming stores, wider or narrower CTAs, two or four blocks a warp at a time gave nothing or
+// cost time.
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -398,15 +398,15 @@ __device__ __forceinline__ void step_block(const Tile<W, GBF16, S8>& tl, int war
   at.template store<FULL>(tl.v, v);
 }
 
-// 16-byte slots of a thread, kThreads apart: the next block's gradient, weights and codes.
+// 16-byte slots of a thread, kThreads apart, of two blocks: their gradient, weights and codes.
 template <int W, bool GBF16>
 struct Ahead {
   static constexpr int kG = GBF16 ? 1 : 2, kP = W == W_BF16 ? 1 : 2;
   static constexpr int kPitch = 16 * kThreads, kBytes = (kG + kP + 1) * kPitch;
-  uint32_t slot;
-  float sm, sv;
+  uint32_t slot;         // of the block taken next; the one behind it is kBytes on or back
+  float2 scales, after;  // theirs
   __device__ explicit Ahead(const char* smem) : slot(smem_addr(smem) + threadIdx.x * 16) {}
-  __device__ void fill(const Tile<W, GBF16, true>& tl, int warp, int lane) {
+  __device__ float2 fill(const Tile<W, GBF16, true>& tl, int warp, int lane, uint32_t slot) const {
     const uint32_t at = warp * kBlock + lane * 8;
     const char* g = reinterpret_cast<const char*>(tl.g + at);
     const char* p = reinterpret_cast<const char*>(tl.weights() + at);
@@ -416,8 +416,7 @@ struct Ahead {
     for (int i = 0; i < kP; ++i) copy_ahead16(slot + (kG + i) * kPitch, p + 16 * i);
     copy_ahead8(slot + (kG + kP) * kPitch, tl.m + at);
     copy_ahead8(slot + (kG + kP) * kPitch + 8, tl.v + at);
-    sm = tl.m_scale[warp];
-    sv = tl.v_scale[warp];
+    return make_float2(tl.m_scale[warp], tl.v_scale[warp]);
   }
   __device__ uint2 codes(uint32_t byte) const {
     uint2 a;
@@ -443,7 +442,7 @@ struct Ahead {
     }
   }
 };
-// or the slots, which take the next block as soon as they have been read.
+// or the slots, which take the block after next as soon as they have been read.
 template <int W, bool GBF16, int CAP>
 struct Copied {
   Ahead<W, GBF16>& from;
@@ -461,19 +460,26 @@ struct Copied {
     const uint2 a = from.codes(8);
     decode8(a.x, a.y, x);
   }
-  __device__ float2 scales(int) const { return make_float2(from.sm, from.sv); }
+  uint32_t stage;
+  __device__ float2 scales(int) const { return from.scales; }
   __device__ void done() const {
     const Tile<W, GBF16, true> next(b, next_item, next_tile);
-    if (next.n == kTile) from.fill(next, warp, lane);
+    from.scales = from.after;
+    if (next.n == kTile) from.after = from.fill(next, warp, lane, from.slot);
+    from.slot += stage;
     commit_copies();
   }
 };
 
+// CTAs of an SM: the registers that keep the row of operations without a spill (8-bit states
+// 80 a thread, with masters more: 201 M weights 582 us at 2 CTAs, 632 with 4 bytes spilled at 3).
+constexpr int ctas_per_sm(int w, bool s8) { return !s8 ? 4 : w == W_BF16_MASTER ? 2 : 3; }
+
 template <int W, bool GBF16, bool S8, int CAP>
-__global__ void __launch_bounds__(kThreads, S8 && W != W_BF16 ? 3 : 4)
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(W, S8))
 adamw_kernel(const __grid_constant__ Batch<CAP> b, const __grid_constant__ Consts c,
              const float* lr_p, const float* grad_scale, int32_t* step, bool last_launch) {
-  __shared__ __align__(16) char smem[S8 ? Ahead<W, GBF16>::kBytes : 16];
+  __shared__ __align__(16) char smem[S8 ? 2 * Ahead<W, GBF16>::kBytes : 16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tiles = b.first_tile[b.count];
   int tile = blockIdx.x;
@@ -484,9 +490,21 @@ adamw_kernel(const __grid_constant__ Batch<CAP> b, const __grid_constant__ Const
     else hi = mid - 1;
   }
   Ahead<W, GBF16> ahead(smem);
+  // the tensor of the tile at or behind `from_item` (tiles only rise)
+  auto item_of = [&](int t, int from_item) {
+    if (t >= tiles) return b.count;
+    while (b.first_tile[from_item + 1] <= t) ++from_item;
+    return from_item;
+  };
+  const int stride = (int)gridDim.x;
+  int next_item = S8 ? item_of(tile + stride, item) : 0;
+  uint32_t stage = Ahead<W, GBF16>::kBytes;
   if constexpr (S8) {
     const Tile<W, GBF16, S8> tl(b, item, tile);
-    if (tl.n == kTile) ahead.fill(tl, warp, lane);
+    if (tl.n == kTile) ahead.scales = ahead.fill(tl, warp, lane, ahead.slot);
+    commit_copies();
+    const Tile<W, GBF16, S8> nx(b, next_item, tile + stride);
+    if (nx.n == kTile) ahead.after = ahead.fill(nx, warp, lane, ahead.slot + stage);
     commit_copies();
   }
   Step st;
@@ -502,15 +520,12 @@ adamw_kernel(const __grid_constant__ Batch<CAP> b, const __grid_constant__ Const
   }
 
   while (tile < tiles) {
-    // tiles only rise, so the next one's tensor is this one's or one behind it
-    const int next = tile + (int)gridDim.x;
-    int next_item = next < tiles ? item : b.count;
-    while (next_item < b.count && b.first_tile[next_item + 1] <= next) ++next_item;
     const Tile<W, GBF16, S8> tl(b, item, tile);
     // a tensor's last tile: block by block, each lane looking after its own elements
     if constexpr (S8) {
-      wait_copies<0>();
-      const Copied<W, GBF16, CAP> copied = {ahead, b, next_item, next, warp, lane};
+      wait_copies<1>();
+      const int then = tile + 2 * stride, then_item = item_of(then, next_item);
+      const Copied<W, GBF16, CAP> copied = {ahead, b, then_item, then, warp, lane, stage};
       if (tl.n == kTile) {
         step_block<W, GBF16, S8, true>(tl, warp, lane, c, st, copied);
       } else {
@@ -519,6 +534,9 @@ adamw_kernel(const __grid_constant__ Batch<CAP> b, const __grid_constant__ Const
           step_block<W, GBF16, S8, false>(tl, warp, lane, c, st,
                                           Direct<W, GBF16, S8, false>(tl, warp, lane));
       }
+      stage = 0u - stage;
+      item = next_item;
+      next_item = then_item;
     } else if (tl.n == kTile) {
       step_block<W, GBF16, S8, true>(tl, warp, lane, c, st,
                                      Direct<W, GBF16, S8, true>(tl, warp, lane));
@@ -526,8 +544,8 @@ adamw_kernel(const __grid_constant__ Batch<CAP> b, const __grid_constant__ Const
       step_block<W, GBF16, S8, false>(tl, warp, lane, c, st,
                                       Direct<W, GBF16, S8, false>(tl, warp, lane));
     }
-    tile = next;
-    item = next_item;
+    tile += stride;
+    if constexpr (!S8) item = item_of(tile, item);
   }
   // The last CTA to end raises the step count: all have read it by then.  The ticket wraps
   // to 0 by itself, so nothing has to be cleared between calls.
@@ -566,7 +584,7 @@ cudaError_t launch_batch(const moet_adamw_tensor* const* ts, int count, const Co
   // fp32 states: up to 16 CTAs one after another in an SM's slot, so that the SMs that memory
   // serves faster take more of the tiles (50 M weights: 197 us, 222 with one CTA a slot that
   // stays).  8-bit states: one that stays, since a CTA's start, with no block copied ahead,
-  // costs more than that gives (402 M weights: 857 us, 930 to 1000 with 4 to 32 a slot).
+  // costs more than that gives (402 M weights: 875 us, 937 with 2 a slot).
   const int per_slot = S8 ? 1 : 16;
   const int most = tiles < cap ? tiles : cap;
   const int turns = tiles / (cap * per_slot) > 1 ? tiles / (cap * per_slot) : 1;
