@@ -8,9 +8,9 @@
 // a sequence's end adds the warps' columns in warp order into one partial row.  Chunk i's
 // part of sequence s goes to row i + s: both only rise along the tokens, and one of them
 // rises from each (chunk, sequence) pair that meets to the next, so no two share a row.
-// Second kernel (the same one, behind a cluster barrier, for a small batch): a CTA per sequence and 32 experts adds that sequence's partial rows in chunk
-// order; the last CTA to end adds the sequences' losses in order.  No atomics on values: the
-// same bits on every run.  The traffic is the logits once (16384 x 256: 2.6 us of HBM); what
+// Second kernel (the same one, behind a cluster barrier, for a small batch): a CTA per sequence
+// and 32 experts adds that sequence's partial rows in chunk order; the last CTA to end adds
+// the sequences' losses in order.  No atomics on values: the same bits on every run.  The traffic is the logits once (16384 x 256: 2.6 us of HBM); what
 // bounds it are the two dependent kernels, each a chain of loads, sums and barriers: 12.9 us
 // at that size, 12.8 us on 24 packed sequences of 128 experts.
 #include "train_common.cuh"
@@ -180,7 +180,7 @@ __device__ __forceinline__ void chunk_sums(const Batch& b, const Workspace& w, c
           if (i > 0) top[u] = fmaxf(top[u], x[u][i]);
         }
         bad_value |= on[u] && zero != 0.f;
-        asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top[u]) : "f"(top[u]));
+        asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top[u]) : "f"(top[u]));
       }
       // e^(x - top) = 2^((x - top) log2 e): the argument's rounding, 2^-24 of it, is a relative
       // error of p that falls as p does, under 2^-22 where p > 1/16

@@ -81,26 +81,38 @@ MOET_HOST int64_t moet_read_arguments(PyObject* list, int64_t count, int32_t dev
   return ARG_OK;
 }
 
-// Gradients for the tensors of an optimizer's step: fp32 or bf16, of sizes[i] elements; their
-// addresses and types go into descriptors[i].g and .g_dtype.  Returns as above (the
-// descriptors before tensor i are filled then, and no step has been made).
-MOET_HOST int64_t moet_read_gradients(PyObject* list, int64_t count, int32_t device,
-                                      const int64_t* sizes, moet_adamw_tensor* descriptors) {
-  if (length(list) != count) return ARG_LIST;
-  int64_t i = 0;
+// The weights and gradients of an optimizer's step: weights of the descriptors' types, gradients
+// fp32 or bf16, each of sizes[i] elements; their addresses (a weight's storage may have been
+// exchanged since the last step) and the gradients' types go into the descriptors.  Returns 0,
+// or 8 i + what is wrong with gradient i, or 8 (count + i) + what is wrong with weight i (the
+// descriptors before it are filled then, and no step has been made).
+MOET_HOST int64_t moet_read_step(PyObject* grads, PyObject* weights, int64_t count,
+                                 int32_t device, const int64_t* sizes,
+                                 moet_adamw_tensor* descriptors) {
+  if (length(grads) != count) return ARG_LIST;
+  if (length(weights) != count) return 8 * count + ARG_LIST;
+  int64_t at = 0;
   try {
-    for (; i < count; ++i) {
-      PyObject* o = item(list, i);
-      if (!THPVariable_Check(o)) return 8 * i + ARG_TYPE;
-      const at::Tensor& t = THPVariable_Unpack(o);
-      const int type = type_of(t);
-      if (type != MOET_F32 && type != MOET_BF16) return 8 * i + ARG_TYPE;
-      if (const int bad = check(t, device, sizes[i], false)) return 8 * i + bad;
-      descriptors[i].g = t.const_data_ptr();
+    for (int64_t i = 0; i < count; ++i) {
+      at = 8 * i;
+      PyObject* o = item(grads, i);
+      if (!THPVariable_Check(o)) return at + ARG_TYPE;
+      const at::Tensor& g = THPVariable_Unpack(o);
+      const int type = type_of(g);
+      if (type != MOET_F32 && type != MOET_BF16) return at + ARG_TYPE;
+      if (const int bad = check(g, device, sizes[i], false)) return at + bad;
+      at = 8 * (count + i);
+      o = item(weights, i);
+      if (!THPVariable_Check(o)) return at + ARG_TYPE;
+      const at::Tensor& p = THPVariable_Unpack(o);
+      if (type_of(p) != descriptors[i].p_dtype) return at + ARG_TYPE;
+      if (const int bad = check(p, device, sizes[i], false)) return at + bad;
+      descriptors[i].g = g.const_data_ptr();
       descriptors[i].g_dtype = type;
+      descriptors[i].p = p.data_ptr();
     }
   } catch (...) {
-    return 8 * i + ARG_TYPE;
+    return at + ARG_TYPE;
   }
   return ARG_OK;
 }

@@ -290,9 +290,11 @@ def _args() -> ctypes.PyDLL:
             raise RuntimeError(f"{ARGS_LIB_PATH} is missing: build it with "
                                "`python -m skew_aware_token_b200.build`")
         handle = ctypes.PyDLL(ARGS_LIB_PATH)  # the interpreter's lock stays held
-        for fn in (handle.moet_read_arguments, handle.moet_read_gradients):
-            fn.restype = ctypes.c_int64
-            fn.argtypes = [ctypes.py_object, ctypes.c_int64, ctypes.c_int32, _VP, _VP]
+        handle.moet_read_arguments.restype = handle.moet_read_step.restype = ctypes.c_int64
+        handle.moet_read_arguments.argtypes = [ctypes.py_object, ctypes.c_int64, ctypes.c_int32,
+                                               _VP, _VP]
+        handle.moet_read_step.argtypes = [ctypes.py_object, ctypes.py_object, ctypes.c_int64,
+                                          ctypes.c_int32, _VP, _VP]
         _args_lib = handle
     return _args_lib
 
@@ -326,20 +328,24 @@ class Arguments:
         return out
 
 
-def read_gradients(grads, sizes, device: int, tensors) -> None:
-    """Checks a list or tuple of gradients (fp32 or bf16, contiguous, sizes[i] elements, on
-    CUDA device `device`) and fills in their addresses and types in the MoetAdamwTensor array
-    `tensors`.  `sizes`: a ctypes array of int64."""
-    rc = _args().moet_read_gradients(grads, len(sizes), device, sizes, tensors)
+def read_step(grads, params, sizes, device: int, tensors) -> None:
+    """Checks the gradients (a list or tuple of fp32 or bf16 tensors, contiguous, of sizes[i]
+    elements, on CUDA device `device`) and weights of an optimizer's step and fills their
+    addresses and the gradients' types into the MoetAdamwTensor array `tensors`.  `sizes`: a
+    ctypes array of int64."""
+    count = len(sizes)
+    rc = _args().moet_read_step(grads, params, count, device, sizes, tensors)
     if rc:
         i, what = divmod(rc, 8)
+        name = f"grads[{i}]" if i < count else f"params[{i - count}]"
         if what == 1:
-            raise ValueError(f"a list of {len(sizes)} gradients is needed")
+            raise ValueError(f"a list of {count} gradients is needed")
         if what == 2:
-            raise TypeError(f"grads[{i}] must be a torch.float32 or torch.bfloat16 tensor")
+            raise TypeError(f"{name} must be a torch.float32 or torch.bfloat16 tensor"
+                            + (" of the type it had" if i >= count else ""))
         if what == 3:
-            raise TypeError(f"grads[{i}] must be on cuda:{device}")
-        raise ValueError(f"grads[{i}] must be contiguous with {sizes[i]} elements")
+            raise TypeError(f"{name} must be on cuda:{device}")
+        raise ValueError(f"{name} must be contiguous with {sizes[i % count]} elements")
 
 
 def call(fn: str, *args) -> None:

@@ -4,15 +4,15 @@ buffers, as MoeLayer does, and calls the library's kernels (include/moeskew_trai
 current CUDA stream of its device, or on `stream`.  One object serves one stream at a time;
 its outputs are views that the next call overwrites.
 
-    norm = BlockNorm(wl, train=True)
+    norm_in, norm_out = BlockNorm(wl, train=True), BlockNorm(wl, train=True)
     router = RouterLoss(wl, n_seq=3)
     opt = AdamW([w1, w2], lr=1e-3, state_bits=8)
     layer = MoeLayer(wl, train=True, o_rows=True)
 
-    _, x = norm(h, w_next=w_in)                        # the norm before the block
+    _, x = norm_in(h, w_next=w_in)                     # the norm before the block
     y = layer(logits, x, w1, w2)
     losses = router(logits, layer.view("topk_ids"), seq_off=seq_off)
-    h_out, _ = norm_out(h, y=y, w_post=w_out)          # behind it (an object of its own)
+    h_out, _ = norm_out(h, y=y, w_post=w_out)          # the norm and residual behind it
     ...
     g = norm_out.backward(h_out, y=y, w_post=w_out, dh_out=dh_out)
     dx, dw1, dw2 = layer.backward(g.dy, w1, w2)
@@ -52,6 +52,12 @@ class _OnDevice:
     def _on(self, device):
         self.device = device
         self._index = device.index
+
+    def _settle(self):
+        """The buffers' first fill is done when the object is, whatever stream it is used on."""
+        with torch.cuda.device(self._index):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
 
     def _call(self, fn, args, stream):
         index = self._index
@@ -113,6 +119,7 @@ class RouterLoss(_OnDevice):
                                                 self.status)]
         self._saved = [t.data_ptr() for t in (self.counts, self.seq_info, self._lse)]
         self._grads = [t.data_ptr() for t in (self._dgates, self._dlogits, self.status)]
+        self._settle()
 
     def __call__(self, logits, topk_ids, token_mask=None, seq_off=None, stream=None):
         """fp32 [2]: balance loss and z loss of logits fp32 [T, E] and the router's topk_ids
@@ -203,6 +210,7 @@ class BlockNorm(_OnDevice):
         self._grad_args = N.Arguments(self._index, *inputs, ("dh_out", h_dtype, rows, True),
                                       ("dx", f32, rows, True))
         self._x = self.x.data_ptr()
+        self._settle()
 
     def __call__(self, h, y=None, gate=None, w_post=None, w_next=None, h_out=None, stream=None):
         """(h_out, x): the residual stream behind the block and, with w_next, the next
@@ -259,7 +267,9 @@ class AdamW(_OnDevice):
     codes with an fp32 scale per 256 elements; `v` then holds the second moment's root).
     `master`: True keeps fp32 masters of bf16 weights, made from the weights here; or a list
     of them.  `m`, `v`, `m_scale`, `v_scale`: lists to take as states (a checkpoint's, or
-    views of a flat buffer); zeros by default.  `step`: steps that they have seen.
+    views of a flat buffer); zeros by default.  `step`: steps that they have seen.  The
+    states stay these tensors (copy into them to restore others); a weight's storage may be
+    exchanged between steps, not its size or type.
 
     Steps taken and learning rate live on the device (`steps`, `lr`), so a captured step
     replays with their current values: set_lr() between replays."""
@@ -267,15 +277,17 @@ class AdamW(_OnDevice):
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay=0.01, state_bits: int = 32, master=None, m=None, v=None,
                  m_scale=None, v_scale=None, step: int = 0):
-        self.params = list(params)
+        self.params = tuple(params)
         if not self.params:
             raise ValueError("no parameters")
+        if not all(isinstance(p, torch.Tensor) for p in self.params):
+            raise TypeError("params must be CUDA tensors")
         if state_bits not in (8, 32):
             raise ValueError("state_bits is 8 or 32")
         if not all(0 <= b < 1 for b in betas) or not eps > 0 or step < 0:
             raise ValueError("betas in [0, 1), eps > 0 and step >= 0 are needed")
         first = self.params[0]
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        if not first.is_cuda:
             raise TypeError("params must be CUDA tensors")
         dev = first.device
         self._on(dev)
@@ -288,16 +300,16 @@ class AdamW(_OnDevice):
         if master is True:
             master = [p.detach().float() if p.dtype is torch.bfloat16 else None
                       for p in self.params]
-        zeros = lambda ns, dt: [torch.zeros(n, dtype=dt, device=dev) for n in ns]
-        self.m = zeros(sizes, state) if m is None else list(m)
-        self.v = zeros(sizes, state) if v is None else list(v)
+        zeros = lambda ns, dt: tuple(torch.zeros(n, dtype=dt, device=dev) for n in ns)
+        self.m = zeros(sizes, state) if m is None else tuple(m)
+        self.v = zeros(sizes, state) if v is None else tuple(v)
         self.m_scale = self.v_scale = None
         if state_bits == 8:
-            self.m_scale = zeros(blocks, torch.float32) if m_scale is None else list(m_scale)
-            self.v_scale = zeros(blocks, torch.float32) if v_scale is None else list(v_scale)
+            self.m_scale = zeros(blocks, torch.float32) if m_scale is None else tuple(m_scale)
+            self.v_scale = zeros(blocks, torch.float32) if v_scale is None else tuple(v_scale)
         elif m_scale is not None or v_scale is not None:
             raise ValueError("scales belong to 8-bit states")
-        self.master = None if master is None else list(master)
+        self.master = None if master is None else tuple(master)
         for name, ts in (("weight_decay", decay), ("m", self.m), ("v", self.v),
                          ("m_scale", self.m_scale), ("v_scale", self.v_scale),
                          ("master", self.master)):
@@ -340,6 +352,7 @@ class AdamW(_OnDevice):
         self._opt = N.MoetAdamw(float(betas[0]), float(betas[1]), float(eps))
         self.lr = torch.full((4,), float(lr), device=dev)
         self.steps = torch.tensor([step, 0, 0, 0], dtype=torch.int32, device=dev)
+        self._settle()
 
     def set_lr(self, lr: float) -> None:
         """Sets the learning rate of the steps that follow on the current stream."""
@@ -350,7 +363,7 @@ class AdamW(_OnDevice):
         fp32 device tensor that multiplies them (a clip or a loss scale's inverse); when it
         is not finite, the step is left out."""
         grads = grads if isinstance(grads, (list, tuple)) else list(grads)
-        N.read_gradients(grads, self._sizes, self._index, self._tensors)
+        N.read_step(grads, self.params, self._sizes, self._index, self._tensors)
         scale = None if grad_scale is None else self._scale_args.read(grad_scale)[0]
         self._call("moet_adamw_step",
                    (self._tensors, len(self._sizes), ctypes.byref(self._opt), self.lr.data_ptr(),

@@ -562,6 +562,46 @@ def test_adamw_on_views_of_flat_storage():
     assert bool((flat["p"].cpu()[gap] == 7).all()) and not flat["m"].float().cpu()[gap].any()
 
 
+def test_adamw_follows_a_weight_whose_storage_is_exchanged():
+    """The step updates what the weight is at the step, and refuses it when it changed size,
+    type or device; the states cannot be exchanged unnoticed."""
+    p = torch.nn.Parameter(torch.ones(1000, device=DEV))
+    opt, g = AdamW([p], lr=LR, weight_decay=0.0), [torch.ones(1000, device=DEV)]
+    old = p.data
+    p.data = torch.full((1000,), 2.0, device=DEV)
+    opt.step(g)
+    assert bool((old == 1).all()) and bool((p.data < 2).all())
+    for bad, error in ((torch.ones(999, device=DEV), ValueError), (torch.ones(1000), TypeError),
+                       (torch.ones(1000, device=DEV).bfloat16(), TypeError)):
+        q = torch.nn.Parameter(torch.ones(1000, device=DEV))
+        opt = AdamW([q], lr=LR)
+        q.data = bad
+        with pytest.raises(error, match=r"params\[0\]"):
+            opt.step(g)
+    with pytest.raises(TypeError):
+        opt.m[0] = torch.zeros(1000, device=DEV)
+
+
+def test_first_use_on_another_stream():
+    """An object used at once on a stream other than the one it was built on."""
+    wl = workload(700, d=1024, E=64, k=8)
+    logits, ids, _ = (t.to(DEV) for t in router_inputs(700, 64, 8))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    want = None
+    for _ in range(5):
+        big = torch.empty(1 << 28, device=DEV)
+        for _ in range(20):
+            big.fill_(1.0)                      # the building stream is busy
+        r = RouterLoss(wl, device=DEV)
+        with torch.cuda.stream(side):
+            r(logits, ids)
+        side.synchronize()
+        got = (r.losses.clone(), r.counts.clone(), r.probs.clone())
+        want = want or got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_adamw_bad_gradients_stay_in_their_block():
     n = 1024
     for bits in (32, 8):

@@ -219,7 +219,7 @@ def test_gradient_lists_are_checked():
             ([torch.zeros(5, device="meta")] * 3, TypeError, r"grads\[0\] must be on"),
             ([torch.zeros(5).to_sparse()] * 3, TypeError, r"grads\[0\] must be on")):
         with pytest.raises(error, match=text):
-            N.read_gradients(bad, sizes, 0, t)
+            N.read_step(bad, host, sizes, 0, t)
     assert all(not e.g for e in t)
 
 
