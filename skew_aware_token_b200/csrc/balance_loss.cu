@@ -292,8 +292,7 @@ __device__ __forceinline__ void sequence_sums(const Batch& b, const Workspace& w
         z += w.zsum[(long long)i + s];
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    n = __reduce_add_sync(0xffffffffu, n);
     z = warp_sum(z);
     __syncthreads();
     s_p[warp][lane] = p;
@@ -350,29 +349,35 @@ __device__ __forceinline__ void batch_sums(const Batch& bt, const Workspace& w,
     n += ns;
     some += ns > 0;
   }
+  auto warp_totals = [&] {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-    z += __shfl_xor_sync(0xffffffffu, z, o);
-    n += __shfl_xor_sync(0xffffffffu, n, o);
-    some += __shfl_xor_sync(0xffffffffu, some, o);
-  }
-  if (lane == 0) {
-    d_b[warp] = b;
-    d_z[warp] = z;
-    i_n[warp] = n;
-    i_s[warp] = some;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < WARPS; ++i) {
-      b += d_b[i];
-      z += d_z[i];
-      n += i_n[i];
-      some += i_s[i];
+    for (int o = 16; o > 0; o >>= 1) {
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+      z += __shfl_xor_sync(0xffffffffu, z, o);
     }
-    out.losses[0] = some > 0 ? (float)(b * E / ((double)k * some)) : 0.f;
-    out.losses[1] = n > 0 ? (float)(z / n) : 0.f;
+    n = __reduce_add_sync(0xffffffffu, n);
+    some = __reduce_add_sync(0xffffffffu, some);
+  };
+  warp_totals();
+  if ((long long)n_seq * n_slices > 32) {  // else the first warp has it all
+    if (lane == 0) {
+      d_b[warp] = b;
+      d_z[warp] = z;
+      i_n[warp] = n;
+      i_s[warp] = some;
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    const bool in = lane < WARPS;
+    b = in ? d_b[lane] : 0.;
+    z = in ? d_z[lane] : 0.;
+    n = in ? i_n[lane] : 0;
+    some = in ? i_s[lane] : 0;
+    warp_totals();
+  }
+  if (threadIdx.x == 0) {
+    out.losses[0] = some > 0 ? (float)b * ((float)E / ((float)k * (float)some)) : 0.f;
+    out.losses[1] = n > 0 ? (float)z / (float)n : 0.f;
     out.seq_info[n_seq] = n;
     out.seq_info[n_seq + 1] = some;
   }
