@@ -62,7 +62,10 @@ def _args_up_to_date() -> bool:
 
 def _build_args() -> None:
     """libmoeskew_args.so: linked to the torch that this interpreter imports."""
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError(f"{ARGS_SOURCE} needs torch's headers: torch is not installed")
+    torch_dir = spec.submodule_search_locations[0]
     include = os.path.join(torch_dir, "include")
     lib = os.path.join(torch_dir, "lib")
     tmp = ARGS_LIB + ".tmp"

@@ -390,6 +390,49 @@ def test_block_norm_gradient(T, d, ht, wt, parts):
     assert all(t is None or torch.equal(t, f) for t, f in zip(run(), first))
 
 
+@pytest.mark.parametrize("T,d,ht", [(5000, 2048, torch.bfloat16), (9000, 512, torch.float32),
+                                    (1500, 8192, torch.float32)])
+def test_block_norm_many_rows(T, d, ht):
+    """Many rows a group, both directions, against the 64-bit form on the GPU."""
+    a = on_gpu(norm_inputs(T, d, ht, torch.float32, "all", seed=40))
+    norm = BlockNorm(workload(T, d=d), h_dtype=ht, train=True, device=DEV, **CONST)
+    q = wide(a)
+    leaf = {n: t.clone().requires_grad_() for n, t in q.items()}
+    want_h, want_x = R.block_norm(leaf["h"], leaf["y"], leaf["gate"], leaf["w_post"],
+                                  leaf["w_next"], **CONST)
+    h_out, x = norm(**a)
+    store = BF16 if ht is torch.bfloat16 else 0.0
+    size = CONST["res_scale"] * q["h"].abs() + (want_h - CONST["res_scale"] * q["h"]).abs()
+    close(h_out, want_h, (store * want_h.abs() + 32 * U * size).detach().cpu(), "h_out")
+    # the gradient at the stream as it is stored
+    stored = h_out.double().requires_grad_()
+    dh_out, dx = torch.randn(T, d, device=DEV).to(ht), torch.randn(T, d, device=DEV)
+    xs = R.rms_norm(stored, leaf["w_next"], CONST["eps"], CONST["w_offset"])
+    gh, gw = torch.autograd.grad((xs * dx.double()).sum(), (stored, leaf["w_next"]))
+    u = dh_out.double() + gh
+    out, _ = R.block_norm(torch.zeros_like(u), leaf["y"], leaf["gate"], leaf["w_post"], None,
+                          **CONST)
+    gy, gg, gp = torch.autograd.grad((out * u).sum(), [leaf[n] for n in ("y", "gate", "w_post")])
+    g = norm.backward(h_out, y=a["y"], gate=a["gate"], w_post=a["w_post"], w_next=a["w_next"],
+                      dh_out=dh_out, dx=dx)
+    # sizes as in test_block_norm_gradient; a CTA adds at most 9000 / 148 rows, 296 CTAs at most
+    A = 1 / torch.sqrt((stored.detach() ** 2).mean(1, keepdim=True) + CONST["eps"])
+    wn, wp = (q[n] + CONST["w_offset"] for n in ("w_next", "w_post"))
+    hs, dxa, ya = stored.detach().abs(), dx.double().abs(), q["y"].abs()
+    M = dh_out.double().abs() + A * dxa * wn.abs() + A ** 3 * hs * (dxa * wn.abs() * hs).mean(
+        1, keepdim=True)
+    ry = 1 / torch.sqrt((q["y"] ** 2).mean(1, keepdim=True) + CONST["eps"])
+    c, gt = abs(CONST["out_scale"]), q["gate"][:, None]
+    ysize = c * gt * ry * M * wp.abs() + c * gt * ry ** 3 * ya * (M * wp.abs() * ya).mean(
+        1, keepdim=True)
+    res = CONST["res_scale"] * u
+    close(g.dh, res, (store * res.abs() + 64 * U * M).cpu(), "dh")
+    close(g.dy, gy, (96 * U * ysize).cpu(), "dy")
+    close(g.dgate, gg, (96 * U * (c * ry * M * wp.abs() * ya).sum(1)).cpu(), "dgate")
+    close(g.dw_next, gw, (192 * U * (dxa * A * hs).sum(0)).cpu(), "dw_next")
+    close(g.dw_post, gp, (192 * U * (c * gt * ry * M * ya).sum(0)).cpu(), "dw_post")
+
+
 def test_block_norm_gradient_parts_and_in_place():
     """dh_out = None is zeros; dh may take dh_out's place (C ABI)."""
     T, d = 77, 768
