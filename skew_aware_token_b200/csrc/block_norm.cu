@@ -134,7 +134,7 @@ __device__ __forceinline__ float group_sum(float v, int W, int group, int warp, 
 // The six sums of a row over its group of W warps, on every thread.  `red`: 8 * 17 floats.
 __device__ __forceinline__ void group_sum8(float (&v)[8], int W, int group, int warp, int lane,
                                            float* red) {
-  float s = warp_sum8(v, lane);
+  float s = warp_sums(v, lane);
   if (W > 1) {
     if ((lane & 3) == 0) red[(lane >> 2) * 17 + warp] = s;
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(W * 32) : "memory");

@@ -33,9 +33,9 @@ __device__ __forceinline__ uint4 ld_once(const uint4* p) {
   return v;
 }
 
-// W warps a token, kEpt experts a thread.  dy == NULL: the losses' part alone; dloss == NULL:
-// the gates' part alone.
-template <int W, int kEpt>
+// W warps a token, kEpt experts a thread, at most K choices a token.  dy == NULL: the losses'
+// part alone; dloss == NULL: the gates' part alone.
+template <int W, int kEpt, int K>
 __global__ void __launch_bounds__(kThreads)
 router_backward_kernel(const RouterArgs a, const float* __restrict__ logits,
                        const int32_t* __restrict__ ids, const float* __restrict__ gates,
@@ -46,7 +46,7 @@ router_backward_kernel(const RouterArgs a, const float* __restrict__ logits,
                        const float* __restrict__ dloss, float* __restrict__ dgates,
                        float* __restrict__ dlogits, int32_t* __restrict__ status) {
   constexpr int kGroups = kThreads / 32 / W;
-  __shared__ float red[kGroups][2][kMaxK + 1][W];
+  __shared__ float red[kGroups][2][K + 1][W];
   const int lane = threadIdx.x & 31;
   const int group = (threadIdx.x >> 5) / W, warp = (threadIdx.x >> 5) % W;
   const int tid = warp * 32 + lane;
@@ -81,7 +81,9 @@ router_backward_kernel(const RouterArgs a, const float* __restrict__ logits,
         x[i] = e < a.E ? __ldg(logits + (long long)t * a.E + e) : 0.f;
       }
     }
-    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float s[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) s[j] = 0.f;
     if (dy) {
       if (lane < a.k) {
         g = __ldg(gates + (long long)t * a.k + lane);
@@ -94,19 +96,19 @@ router_backward_kernel(const RouterArgs a, const float* __restrict__ logits,
       } else {
         my_row = -1;
       }
-      int row[kMaxK];
+      int row[K];
 #pragma unroll
-      for (int j = 0; j < kMaxK; ++j) row[j] = __shfl_sync(0xffffffffu, my_row, j);
+      for (int j = 0; j < K; ++j) row[j] = __shfl_sync(0xffffffffu, my_row, j);
       for (int v = tid; v < a.d8; v += 32 * W) {
-        uint4 r[kMaxK];
+        uint4 r[K];
 #pragma unroll
-        for (int j = 0; j < kMaxK; ++j)
+        for (int j = 0; j < K; ++j)
           r[j] = row[j] >= 0 ? ld_once(o + (long long)row[j] * a.d8 + v)
                              : make_uint4(0, 0, 0, 0);
         float g8[8];
         load8(dy + ((long long)t * a.d8 + v) * 8, g8);
 #pragma unroll
-        for (int j = 0; j < kMaxK; ++j) {
+        for (int j = 0; j < K; ++j) {
           float f[8];
           bf16x8_to_f32(r[j], f);
 #pragma unroll
@@ -144,19 +146,19 @@ router_backward_kernel(const RouterArgs a, const float* __restrict__ logits,
       }
     }
     dot = warp_sum(dot);
-    float sum = warp_sum8(s, lane);  // lane l: product l / 4
+    float sum = warp_sums(s, lane);  // lane l: product l / (32 / K)
     if (W > 1) {
-      if ((lane & 3) == 0) red[group][turn][lane >> 2][warp] = sum;
-      if (lane == 0) red[group][turn][kMaxK][warp] = dot;
+      if (lane % (32 / K) == 0) red[group][turn][lane / (32 / K)][warp] = sum;
+      if (lane == 0) red[group][turn][K][warp] = dot;
       asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(W * 32) : "memory");
       sum = dot = 0.f;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        dot += red[group][turn][kMaxK][w];
-        if (lane < kMaxK) sum += red[group][turn][lane][w];
+        dot += red[group][turn][K][w];
+        if (lane < K) sum += red[group][turn][lane][w];
       }
     } else {
-      sum = __shfl_sync(0xffffffffu, sum, (lane * 4) & 31);  // lane j: product j
+      sum = __shfl_sync(0xffffffffu, sum, lane * (32 / K) & 31);  // lane j: product j
     }
     float out[kEpt];
 #pragma unroll
@@ -166,7 +168,7 @@ router_backward_kernel(const RouterArgs a, const float* __restrict__ logits,
       const float add = g * (sum - mean);
       if (dgates && warp == 0 && lane < a.k) dgates[(long long)t * a.k + lane] = sum;
 #pragma unroll
-      for (int j = 0; j < kMaxK; ++j) {
+      for (int j = 0; j < K; ++j) {
         const int e = __shfl_sync(0xffffffffu, id, j);
         const float to = __shfl_sync(0xffffffffu, add, j);
 #pragma unroll
@@ -208,27 +210,33 @@ cudaError_t launch_router_backward(const moe_cfg& c, const float* logits, const 
         counts, seq_info, lse, dloss, dgates, dlogits, status);
     return cudaGetLastError();
   };
+  auto choices = [&](auto w, auto ept) {
+    constexpr int W = decltype(w)::value, kEpt = decltype(ept)::value;
+    if (c.k <= 2 || !dy) return run(router_backward_kernel<W, kEpt, 2>, W);
+    if (c.k <= 4) return run(router_backward_kernel<W, kEpt, 4>, W);
+    return run(router_backward_kernel<W, kEpt, 8>, W);
+  };
   auto warps = [&](auto w) {
     constexpr int W = decltype(w)::value;
     const int ept = (c.E + 32 * W - 1) / (32 * W);
     if constexpr (W <= 1)
-      if (ept > 4) return run(router_backward_kernel<W, 8>, W);
+      if (ept > 4) return choices(w, std::integral_constant<int, 8>());
     if constexpr (W <= 2)
-      if (ept > 2) return run(router_backward_kernel<W, 4>, W);
+      if (ept > 2) return choices(w, std::integral_constant<int, 4>());
     if constexpr (W <= 2)
-      if (ept > 1) return run(router_backward_kernel<W, 2>, W);
-    return run(router_backward_kernel<W, 1>, W);
+      if (ept > 1) return choices(w, std::integral_constant<int, 2>());
+    return choices(w, std::integral_constant<int, 1>());
   };
   // Warps a token, by the 16-byte loads that a token is (k rows of O, twice that of dy) and
   // the tokens there are.  Measured us, 1 | 2 | 8 warps a token: 16384 tokens of 8 x 2048
-  // (2560 loads) 149 | 141 | 119, 1 token of 8 x 7168 37 | 10 | 5; below that the end of a token
-  // costs more than its rows, and fewer warps share it: 16384 of 4 x 512 28 | 31 | 74, of
-  // 2 x 4096 97 | 96 | 130, but with few tokens a second warp still finds an idle SM: 2048 of
-  // 4 x 1024 10.3 | 7.4 | 11.7, 1111 of 4 x 512 4.2 | 3.7 | 6.7.
-  const int loads = a.d8 * (c.k + 2);
-  if (loads >= 2560 || (loads && c.T < num_sms()))
-    return warps(std::integral_constant<int, 8>());
-  if (c.T < num_sms() * 32) return warps(std::integral_constant<int, 2>());
+  // (2560 loads) 151 | 141 | 119, 4096 of them 41 | 42 | 34, 1 token of 8 x 7168 39 | 11 | 5;
+  // below that the end of a token costs more than its rows and fewer warps share it: 16384 of
+  // 8 x 1024 (1280) 80 | 77 | 95, of 2 x 4096 105 | 99 | 116, of 4 x 512 (384) 27 | 29 | 85, 4096
+  // of them 6.9 | 8.4 | 21; with few tokens a second warp finds an idle SM: 2048 of 4 x 1024
+  // 9.8 | 6.8 | 12.3, 1111 of 4 x 512 4.0 | 3.5 | 6.1.
+  const int loads = a.d8 * (c.k + 2), sms = num_sms();
+  if (loads >= 2560 || (loads && c.T < sms)) return warps(std::integral_constant<int, 8>());
+  if (loads >= 1024 || c.T < sms * 16) return warps(std::integral_constant<int, 2>());
   return warps(std::integral_constant<int, 1>());
 }
 

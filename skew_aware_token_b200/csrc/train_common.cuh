@@ -95,12 +95,13 @@ __device__ __forceinline__ uint4 slot16(uint32_t a) {
   return v;
 }
 
-// Sums of up to 8 values over the warp with 9 shuffles: each of the first three exchanges
-// halves the number of values a lane still carries.  Lane l returns the sum of value l / 4.
-__device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
+// Sums of N = 2, 4 or 8 values over the warp, of 8 with 9 shuffles: each of the first log2 N
+// exchanges halves the number of values a lane still carries.  Lane l returns the sum of value
+// l / (32 / N).
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
 #pragma unroll
-  for (int half = 4; half >= 1; half >>= 1) {
-    const int off = half * 4;
+  for (int half = N / 2, off = 16; half >= 1; half >>= 1, off >>= 1) {
     const bool up = lane & off;
 #pragma unroll
     for (int i = 0; i < half; ++i) {
@@ -108,8 +109,10 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
       v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
     }
   }
-  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
-  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+#pragma unroll
+  for (int off = 16 / N; off >= 1; off >>= 1)
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+  return v[0];
 }
 
 // ---- launches that overlap their predecessor's end (programmatic dependent launch) ----
