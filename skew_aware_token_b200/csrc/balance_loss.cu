@@ -11,8 +11,8 @@
 // Second kernel (the same one, behind a cluster barrier, for a small batch): a CTA per sequence
 // and 32 experts adds that sequence's partial rows in chunk order; the last CTA to end adds
 // the sequences' losses in order.  No atomics on values: the same bits on every run.  The traffic is the logits once (16384 x 256: 2.6 us of HBM); what
-// bounds it are the two dependent kernels, each a chain of loads, sums and barriers: 12.9 us
-// at that size, 12.8 us on 24 packed sequences of 128 experts.
+// bounds it are the two dependent kernels, each a chain of loads, sums and barriers: 12.6 us
+// at that size, 12.3 us on 24 packed sequences of 128 experts.
 #include "train_common.cuh"
 
 namespace moe {
@@ -428,7 +428,7 @@ template <int EPL>
 cudaError_t launch(const Batch& b, const Workspace& w, const Results& r, cudaStream_t st) {
   constexpr int TPW = EPL <= 2 ? 4 : 2;
   const long long units = (long long)b.n_seq * b.n_slices;
-  // A small batch of few sequences takes one launch: 256 tokens of 8 experts 6.7 us against
+  // A small batch of few sequences takes one launch: 256 tokens of 8 experts 6.1 us against
   // 8.2 us in two launches; from 512 tokens on (8.3 against 8.0 us) the chunks of 8 CTAs are
   // too long.
   if (b.T <= kSmallTokens && units <= kCluster * 4) {

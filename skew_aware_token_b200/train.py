@@ -91,15 +91,15 @@ class RouterLoss(_OnDevice):
         self._cfg = ctypes.byref(self.cfg)
         T, E, k, S = self.cfg.T, self.cfg.E, self.cfg.k, self.n_seq
         z = lambda *shape, dt=torch.float32: torch.zeros(shape, dtype=dt, device=dev)
-        self.losses = z(2)
-        self.counts = z(S, E, dt=torch.int32)
-        self.probs = z(S, E)
-        self.seq_info = z(S + 2, dt=torch.int32)
-        self._lse, self._dgates, self._dlogits = z(max(T, 1)), z(max(T * k, 1)), z(max(T * E, 1))
+        new = lambda *shape, dt=torch.float32: torch.empty(shape, dtype=dt, device=dev)
+        self.losses, self.probs = new(2), new(S, E)
+        self.counts, self.seq_info = z(S, E, dt=torch.int32), z(S + 2, dt=torch.int32)
+        self._lse = z(max(T, 1))
+        self._dgates, self._dlogits = new(max(T * k, 1)), new(max(T * E, 1))
         self.lse = self._lse[:T]
         self.dgates = self._dgates[:T * k].view(T, k)
         self.dlogits = self._dlogits[:T * E].view(T, E)
-        self.workspace = z(size, dt=torch.uint8)
+        self.workspace = new(size, dt=torch.uint8)
         self.status = z(4, dt=torch.int32)
         f32, i32, rows = torch.float32, torch.int32, N.moe_workspace_size(self.cfg, N.MOE_WS_ROWS)
         batch = (("token_mask", torch.uint8, T, True), ("seq_off", i32, S + 1, S == 1))
@@ -194,7 +194,7 @@ class BlockNorm(_OnDevice):
         self.h_dtype, self.w_dtype, self.train = h_dtype, w_dtype, bool(train)
         self.norm = N.MoetNorm(eps, w_offset, res_scale, out_scale, _TYPES[h_dtype],
                                _TYPES[w_dtype])
-        new = lambda dt, *shape: torch.zeros(shape, dtype=dt, device=dev)
+        new = lambda dt, *shape: torch.empty(shape, dtype=dt, device=dev)
         rows = max(T, 1)
         self.h_out, self.x = new(h_dtype, rows, d)[:T], new(torch.bfloat16, rows, d)[:T]
         if train:
@@ -315,7 +315,7 @@ class AdamW(_OnDevice):
                          ("master", self.master)):
             if ts is not None and len(ts) != count:
                 raise ValueError(f"{name}: {len(ts)} of them for {count} parameters")
-        spans = []
+        specs, tensors = [], []
         self._tensors = (N.MoetAdamwTensor * count)()
         for i, p in enumerate(self.params):
             if p.dtype not in (torch.float32, torch.bfloat16):
@@ -330,19 +330,17 @@ class AdamW(_OnDevice):
                     raise ValueError("fp32 weights have no master")
                 own.append(("master", w, torch.float32, sizes[i]))
             own.append(("params", p, p.dtype, sizes[i]))
-            N.Arguments(dev.index, *[(f"{name}[{i}]", dt, n, False) for name, _, dt, n in own]
-                        ).read(*[t for _, t, _, _ in own])
-            for name, t, dt, n in own:
-                if n:
-                    spans.append((t.data_ptr(), t.data_ptr() + n * t.element_size(),
-                                  f"{name}[{i}]"))
+            specs += [(f"{name}[{i}]", dt, n, False) for name, _, dt, n in own]
+            tensors += [t for _, t, _, _ in own]
             e = self._tensors[i]
-            e.p, e.m, e.v = p.data_ptr(), self.m[i].data_ptr(), self.v[i].data_ptr()
-            if state_bits == 8:
-                e.m_scale, e.v_scale = self.m_scale[i].data_ptr(), self.v_scale[i].data_ptr()
-            e.master = None if w is None else w.data_ptr()
             e.n, e.weight_decay = sizes[i], decay[i]
             e.p_dtype, e.state_dtype = _TYPES[p.dtype], _TYPES[state]
+        spans = []
+        for (name, dt, n, _), at in zip(specs, N.Arguments(dev.index, *specs).read(*tensors)):
+            field, i = name[:-1].split("[")
+            setattr(self._tensors[int(i)], "p" if field == "params" else field, at)
+            if n:
+                spans.append((at, at + n * dt.itemsize, name))
         spans.sort()
         for (_, end, a), (begin, _, b) in zip(spans, spans[1:]):
             if begin < end:
