@@ -81,10 +81,10 @@ __device__ __forceinline__ void decode8(uint32_t lo, uint32_t hi, float2 (&v)[4]
   }
 }
 
-// A lane's 8 elements of a block, as 4 pairs.  With 8-bit states they are consecutive (one
-// load of 8 codes, one or two of the rest); with fp32 states two runs of 4, one in either
-// half of the block, so that the loads of 16 bytes stay consecutive over the lanes.
-// FULL: the whole block lies inside the tensor.
+// A lane's 8 elements of a block, as 4 pairs.  With 8-bit states they are consecutive (8 codes
+// in one access); with fp32 states two runs of 4, one in either half of the block, so that the
+// accesses of 16 bytes stay consecutive over the lanes.
+// FULL: the whole block lies inside the tensor (an 8-bit one then comes from the slots).
 template <bool S8>
 struct Lane {
   uint32_t at, n;  // the lane's first element, and the elements there are, from the tile's first
@@ -109,15 +109,9 @@ struct Lane {
   template <bool FULL>
   __device__ void load(const __nv_bfloat16* p, float2 (&v)[4]) const {
     if constexpr (FULL) {
-      uint4 a;
-      if constexpr (S8) {
-        a = *reinterpret_cast<const uint4*>(p + at);
-      } else {
-        const uint2 lo = *reinterpret_cast<const uint2*>(p + at);
-        const uint2 hi = *reinterpret_cast<const uint2*>(p + index(4));
-        a = make_uint4(lo.x, lo.y, hi.x, hi.y);
-      }
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+      const uint2 lo = *reinterpret_cast<const uint2*>(p + at);
+      const uint2 hi = *reinterpret_cast<const uint2*>(p + index(4));
+      const uint32_t w[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = bf16_pair(w[i]);
     } else {
@@ -130,15 +124,11 @@ struct Lane {
   }
   template <bool FULL>
   __device__ void load(const uint8_t* p, float2 (&v)[4]) const {
+    static_assert(!FULL, "whole 8-bit blocks come from the slots");
     uint32_t w[2] = {0, 0};
-    if constexpr (FULL) {
-      const uint2 a = *reinterpret_cast<const uint2*>(p + at);
-      w[0] = a.x, w[1] = a.y;
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (index(i) < n) w[i / 4] |= (uint32_t)p[index(i)] << (8 * (i % 4));
-    }
+    for (int i = 0; i < 8; ++i)
+      if (index(i) < n) w[i / 4] |= (uint32_t)p[index(i)] << (8 * (i % 4));
     decode8(w[0], w[1], v);
   }
   template <bool FULL>

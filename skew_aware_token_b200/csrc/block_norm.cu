@@ -6,7 +6,7 @@
 // One pass: a row lives in the registers of a group of warps (units of 4 columns, two a thread),
 // so h, y and the weights are read once and h' and x are written once; the two means are two
 // reductions over the group.  A persistent group copies its next row to shared memory while it
-// works on this one.  Bound by HBM: 16384 x 7168 with an fp32 stream 265 us (1.64 GB, 6.2
+// works on this one.  Bound by HBM: 16384 x 7168 with an fp32 stream 262 us (1.64 GB, 6.3
 // TB/s; a copy of as many bytes takes 251), 4096 x 2048 in bf16 17 us (12.8).
 //
 // The gradient needs six sums of a row, and by linearity one reduction for all of them: with
@@ -16,7 +16,7 @@
 // gradients are kept per column in registers over all rows of a CTA, written as one partial
 // row per CTA, and added over the CTAs in a fixed order by a second kernel.  128 registers a
 // thread without a spill: a few spilled ones in the row loop cost half of the rate.
-// 16384 x 7168 in bf16 takes 361 us (2.11 GB, 5.9 TB/s; a copy of as many bytes 323); what it
+// 16384 x 7168 in bf16 takes 355 us (2.11 GB, 6.0 TB/s; a copy of as many bytes 323); what it
 // waits for most are shared memory and the reduction's shuffles.
 #include "train_common.cuh"
 
