@@ -56,6 +56,9 @@ LOSS_CASES = [
     (515, 60, 6, [0, 515], "none"), (640, 128, 8, list(range(0, 641, 5)), "some"),
     (100, 256, 8, list(range(101)), "none"), (2048, 64, 8, [0, 31, 33, 64, 2048], "some"),
     (300, 200, 5, [0, 100, 200, 300], "all"), (33, 96, 2, [33, 33], "none"),
+    # more sequences than tokens, most of them empty; a batch longer than a chunk's share
+    (70, 16, 2, [0] * 700 + sorted([7 * i // 100 for i in range(900)]) + [63] * 1500, "some"),
+    (9500, 40, 3, [2, 31, 5000, 5000, 9400], "some"),
 ]
 
 
