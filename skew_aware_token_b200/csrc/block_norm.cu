@@ -120,8 +120,10 @@ constexpr int kThreads = 512;       // of a CTA with several row groups, or of t
 constexpr int kFwdRed = 2 * 32;     // floats of a group's reduction buffers
 constexpr int kBwdRed = 2 * 8 * 17;
 
-// The sum over the group of one value, on every thread.  `red` is one of the group's buffers;
-// a caller uses two in turn, so one barrier a sum is enough.
+// The sum over the group of one value, on every thread.  `red` is one of the group's two
+// buffers, which a caller alternates from sum to sum, whichever sums its rows take: a warp that
+// writes a buffer again has passed the barrier of the sum between, which the others reach only
+// when they have read this one.  So one barrier a sum is enough.
 __device__ __forceinline__ float group_sum(float v, int W, int group, int warp, int lane,
                                            float* red) {
   v = warp_sum(v);
@@ -182,7 +184,7 @@ block_norm_kernel(const NormArgs a, const HT* h, const float* __restrict__ y,
     commit_copies();
   };
   const int step = gridDim.x * groups;
-  int t = blockIdx.x * groups + group;
+  int t = blockIdx.x * groups + group, turn = 0;
   ahead(t);
   float wp[U][4], wn[U][4];
 #pragma unroll
@@ -211,7 +213,8 @@ block_norm_kernel(const NormArgs a, const HT* h, const float* __restrict__ y,
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             if (unit(i) < a.d4) s = fmaf(yu[i][j], yu[i][j], s);
-        s = group_sum(s, a.W, group, warp, lane, red);
+        s = group_sum(s, a.W, group, warp, lane, red + turn * (kFwdRed / 2));
+        turn ^= 1;
         scale *= rsqrtf(fmaf(s, a.inv_d, a.eps));
       }
 #pragma unroll
@@ -234,7 +237,8 @@ block_norm_kernel(const NormArgs a, const HT* h, const float* __restrict__ y,
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (unit(i) < a.d4) s = fmaf(hv[i][j], hv[i][j], s);
-      s = group_sum(s, a.W, group, warp, lane, red + kFwdRed / 2);
+      s = group_sum(s, a.W, group, warp, lane, red + turn * (kFwdRed / 2));
+      turn ^= 1;
       const float r = rsqrtf(fmaf(s, a.inv_d, a.eps));
 #pragma unroll
       for (int i = 0; i < U; ++i) {

@@ -436,6 +436,75 @@ def test_block_norm_many_rows(T, d, ht):
     close(g.dw_post, gp, (192 * U * (c * gt * ry * M * ya).sum(0)).cpu(), "dw_post")
 
 
+@pytest.mark.parametrize("parts", PARTS[1:])
+@pytest.mark.parametrize("T,d,ht", [(5000, 2048, torch.bfloat16), (9000, 512, torch.float32),
+                                    (1500, 8192, torch.float32), (2500, 4104, torch.bfloat16)])
+def test_block_norm_many_rows_of_parts(T, d, ht, parts):
+    """Many rows a group where a row takes one sum or none (the norm before the first block,
+    the one behind the last), both directions, and the same bits on every run."""
+    a = on_gpu(norm_inputs(T, d, ht, torch.float32, parts, seed=60))
+    norm = BlockNorm(workload(T, d=d), h_dtype=ht, train=True, device=DEV, **CONST)
+    q = wide(a)
+    leaf = {n: None if t is None else t.clone().requires_grad_() for n, t in q.items()}
+    want_h, want_x = R.block_norm(leaf["h"], leaf["y"], leaf["gate"], leaf["w_post"],
+                                  leaf["w_next"], **CONST)
+    h_out, x = norm(**a)
+    first = [t.clone() for t in (h_out, x) if t is not None]
+    # bounds as in test_block_norm
+    store = BF16 if ht is torch.bfloat16 else 0.0
+    size = q["h"].abs()
+    if a["y"] is not None:
+        size = CONST["res_scale"] * size + (want_h - CONST["res_scale"] * q["h"]).abs()
+        close(h_out, want_h, (store * want_h.abs() + 32 * U * size).detach().cpu(), "h_out")
+    if a["w_next"] is not None:
+        r = 1 / torch.sqrt((want_h ** 2).mean(1, keepdim=True) + CONST["eps"])
+        x_size = want_x.abs() + size * r * (q["w_next"] + CONST["w_offset"]).abs()
+        close(x, want_x, (BF16 * want_x.abs() + 64 * U * x_size).detach().cpu(), "x")
+    for _ in range(20):
+        assert all(torch.equal(t, f) for t, f in
+                   zip([t for t in norm(**a) if t is not None], first))
+    # the gradient at the stored stream, bounds as in test_block_norm_many_rows
+    stored = h_out.double().requires_grad_()
+    dh_out = torch.randn(T, d, generator=gen(61)).to(ht).to(DEV)
+    dx = None if a["w_next"] is None else torch.randn(T, d, generator=gen(62)).to(DEV)
+    run = lambda: norm.backward(h_out, y=a["y"], gate=a["gate"], w_post=a["w_post"],
+                                w_next=a["w_next"], dh_out=dh_out, dx=dx)
+    g = run()
+    u, M = dh_out.double(), dh_out.double().abs()
+    if dx is not None:
+        xs = R.rms_norm(stored, leaf["w_next"], CONST["eps"], CONST["w_offset"])
+        gh, gw = torch.autograd.grad((xs * dx.double()).sum(), (stored, leaf["w_next"]))
+        A = 1 / torch.sqrt((stored.detach() ** 2).mean(1, keepdim=True) + CONST["eps"])
+        hs, qa = stored.detach().abs(), dx.double().abs() * (q["w_next"] + CONST["w_offset"]).abs()
+        u = u + gh
+        M = M + A * qa + A ** 3 * hs * (qa * hs).mean(1, keepdim=True)
+        close(g.dw_next, gw, (192 * U * (dx.double().abs() * A * hs).sum(0)).cpu(), "dw_next")
+    res = u if a["y"] is None else CONST["res_scale"] * u
+    close(g.dh, res, (store * res.abs() + 64 * U * M).cpu(), "dh")
+    if a["y"] is not None:
+        names = [n for n in ("y", "gate", "w_post") if a[n] is not None]
+        out, _ = R.block_norm(torch.zeros_like(u), leaf["y"], leaf["gate"], leaf["w_post"], None,
+                              **CONST)
+        grads = dict(zip(names, torch.autograd.grad((out * u).sum(), [leaf[n] for n in names])))
+        ya, ry, wp = q["y"].abs(), torch.ones(T, 1, device=DEV).double(), 1.0
+        if a["w_post"] is not None:
+            ry = 1 / torch.sqrt((q["y"] ** 2).mean(1, keepdim=True) + CONST["eps"])
+            wp = (q["w_post"] + CONST["w_offset"]).abs()
+        gt = 1.0 if a["gate"] is None else q["gate"][:, None]
+        c = abs(CONST["out_scale"])
+        ysize = c * gt * ry * M * wp
+        if a["w_post"] is not None:
+            ysize = ysize + c * gt * ry ** 3 * ya * (M * wp * ya).mean(1, keepdim=True)
+            close(g.dw_post, grads["w_post"],
+                  (192 * U * (c * gt * ry * M * ya).sum(0)).cpu(), "dw_post")
+        close(g.dy, grads["y"], (96 * U * ysize).cpu(), "dy")
+        if a["gate"] is not None:
+            close(g.dgate, grads["gate"], (96 * U * (c * ry * M * wp * ya).sum(1)).cpu(), "dgate")
+    first = [t.clone() for t in g if t is not None]
+    for _ in range(5):
+        assert all(torch.equal(t, f) for t, f in zip([t for t in run() if t is not None], first))
+
+
 def test_block_norm_gradient_parts_and_in_place():
     """dh_out = None is zeros; dh may take dh_out's place (C ABI)."""
     T, d = 77, 768
