@@ -87,11 +87,14 @@ class MoeLayer:
         self.y = z(max(T * d, 4), dt=f32)
         self.o_rows = (T * d * 4 >= O_ROWS_MIN_Y_BYTES) if o_rows is None else bool(o_rows)
         self.o = z(max(R * d, 8), dt=torch.bfloat16) if (write_o or self.o_rows) else None
+        # whether `o` holds the rows of the batch that the row maps are of
+        self._o_written = False
         self.device = dev
         self._side = torch.cuda.Stream(dev) if dev.type == "cuda" else None
 
     # ------------------------------------------------------------------ stages
     def route(self, logits, stream=None):
+        self._o_written = False
         N.moe_route_hist(self.cfg, logits, self.topk_ids, self.topk_gates, self.counts,
                          self.sumsq, self.kappa, self.status, stream)
 
@@ -110,6 +113,7 @@ class MoeLayer:
 
     def dispatch(self, x, stream=None):
         """Row maps (and, without gather_x, the dispatched rows Xp)."""
+        self._o_written = False
         N.moe_dispatch_permute(self.cfg, x, self.topk_ids, self.topk_gates, self.block_off,
                                self.xp, self.row_token, self.row_gate, self.tok_row,
                                self.status, stream)
@@ -135,9 +139,11 @@ class MoeLayer:
             src = self.xp
         if self.train:
             mode |= N.MOE_FFN_SAVE_Z
+        self._o_written = False
         N.moe_expert_ffn(self.cfg, src, w1, w2, self.tiles, self.plan_info,
                          self.row_token, self.row_gate, mode, self.a_scratch, out,
                          self.status, stream)
+        self._o_written = bool(mode & N.MOE_FFN_WRITE_O)
 
     def combine(self, stream=None, y=None):
         N.moe_combine(self.cfg, self.o, self.tok_row, self.topk_gates,
@@ -190,11 +196,17 @@ class MoeLayer:
     def router_backward(self, router, logits, dy, dloss=None, token_mask=None, seq_off=None,
                         stream=None):
         """Gradient of the router's logits for dL/dy = dy after a forward call of this layer
-        that wrote O rows, plus that of `router`'s losses (train.RouterLoss) with dloss:
-        dlogits fp32 [T, E], a view of router's buffer."""
-        if self.o is None or not self.o_rows:
+        that wrote O rows (refused after one that did not), plus that of `router`'s losses
+        (train.RouterLoss) with dloss: dlogits fp32 [T, E], a view of router's buffer.  A
+        forward in a CUDA graph of the caller's counts when it is captured, not when it is
+        replayed (LayerGraph counts its replays)."""
+        if self.o is None:
             raise ValueError("the gates' gradient reads the expert output rows: build the "
                              "layer with o_rows=True")
+        if not self._o_written:
+            raise ValueError("the gates' gradient reads the expert output rows, which the "
+                             "layer's last forward call did not write (o_rows=True or "
+                             "MOE_FFN_WRITE_O, and not MOE_FFN_ONE_LAUNCH)")
         return router.backward(logits, self.topk_ids, self.topk_gates, dloss=dloss, dy=dy,
                                o=self.o, tok_row=self.tok_row, token_mask=token_mask,
                                seq_off=seq_off, stream=stream)
@@ -278,9 +290,11 @@ class LayerGraph:
         self.graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(self.graph):
             run()
+        self._o_written = layer._o_written
 
     def replay(self):
         self.graph.replay()
+        self.layer._o_written = self._o_written
 
 
 class HostPipeline:

@@ -20,7 +20,7 @@ import torch
 import train_oracle as R
 from skew_aware_token_b200 import native as N
 from skew_aware_token_b200 import synth
-from skew_aware_token_b200.layer import MoeLayer
+from skew_aware_token_b200.layer import LayerGraph, MoeLayer
 from skew_aware_token_b200.synth import WORKLOADS, Workload
 from skew_aware_token_b200.train import AdamW, BlockNorm, RouterLoss
 
@@ -155,6 +155,37 @@ def test_layer_without_o_rows_refuses_the_router_gradient():
     layer = MoeLayer(wl, DEV, train=True, o_rows=False)
     with pytest.raises(ValueError, match="o_rows"):
         layer.router_backward(RouterLoss(wl, device=DEV), None, torch.zeros(wl.T, wl.d, device=DEV))
+
+
+def test_router_gradient_after_other_forwards():
+    """Refused after a forward that wrote no O rows; a layer that holds an O buffer gives its
+    gradient after a call that wrote them; replays of a layer's graph count as its forward."""
+    wl = WORKLOADS["tiny"]
+    w1, w2 = synth.make_weights(wl, DEV)
+    logits, x = synth.make_logits(wl).to(DEV), synth.make_x(wl).to(DEV)
+    dy = torch.ones(wl.T, wl.d, device=DEV)
+    router = RouterLoss(wl, device=DEV)
+    layer = MoeLayer(wl, DEV, train=True, o_rows=True)
+    layer(logits, x, w1, w2)
+    want = layer.router_backward(router, logits, dy).clone()
+    layer(logits, x, w1, w2, mode=N.MOE_FFN_ONE_LAUNCH)
+    with pytest.raises(ValueError, match="o_rows"):
+        layer.router_backward(router, logits, dy)
+    other = MoeLayer(wl, DEV, train=True, write_o=True, o_rows=False)
+    other(logits, x, w1, w2, mode=N.MOE_FFN_WRITE_O)
+    assert torch.equal(other.router_backward(router, logits, dy), want)
+    rows = LayerGraph(layer, w1, w2)
+    fused = LayerGraph(layer, w1, w2, mode=N.MOE_FFN_ONE_LAUNCH)
+    for g in (rows, fused):
+        g.logits.copy_(logits)
+        g.x.copy_(x)
+    fused.replay()
+    with pytest.raises(ValueError, match="o_rows"):
+        layer.router_backward(router, logits, dy)
+    rows.replay()
+    assert torch.equal(layer.router_backward(router, logits, dy), want)
+    torch.cuda.synchronize()
+    assert layer.read_status() == 0 and other.read_status() == 0
 
 
 def test_block_gradients_replayed_from_a_graph():

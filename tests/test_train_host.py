@@ -205,6 +205,46 @@ def test_classes_refuse_the_cpu():
         train.BlockNorm(wl, h_dtype=torch.float16)
 
 
+def test_router_gradient_wants_the_last_forwards_rows(monkeypatch):
+    """A layer's router gradient runs after a forward that wrote O rows, and is refused before
+    any, after one that wrote none, and once the next batch has been routed."""
+    from skew_aware_token_b200.layer import MoeLayer
+    for name in ("moe_route_hist", "moe_block_offsets", "moe_plan_blocks", "moe_combine",
+                 "moe_dispatch_permute", "moe_expert_ffn"):
+        monkeypatch.setattr(N, name, lambda *a, **kw: None)
+    taken = []
+
+    class Router:
+        def backward(self, *a, **kw):
+            taken.append(kw["o"])
+
+    refused = lambda: pytest.raises(ValueError, match="o_rows")
+    go = lambda layer: layer.router_backward(Router(), None, None)
+    forward = lambda layer, mode: layer(None, None, None, None, mode=mode, stream=1)
+    fused, one, wide = N.MOE_FFN_FUSED_COMBINE, N.MOE_FFN_ONE_LAUNCH, N.MOE_FFN_WRITE_O
+    layer = MoeLayer(WORKLOADS["tiny"], "cpu", train=True, o_rows=True)
+    with refused():
+        go(layer)                               # no forward yet
+    forward(layer, fused)
+    go(layer)
+    assert taken[-1] is layer.o
+    forward(layer, one)                         # fuses the combine whatever o_rows says
+    with refused():
+        go(layer)
+    forward(layer, fused)
+    go(layer)
+    layer.pre_ffn(None, None, stream=1)         # the next batch's row maps
+    with refused():
+        go(layer)
+    layer = MoeLayer(WORKLOADS["tiny"], "cpu", train=True, write_o=True, o_rows=False)
+    forward(layer, wide)
+    go(layer)
+    assert len(taken) == 3 and taken[-1] is layer.o
+    forward(layer, fused)
+    with refused():
+        go(layer)
+
+
 def test_gradient_lists_are_checked():
     """The native reader of gradient lists refuses what is not a list of the right tensors and
     says which one it is."""
