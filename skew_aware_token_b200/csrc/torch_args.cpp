@@ -81,38 +81,79 @@ MOET_HOST int64_t moet_read_arguments(PyObject* list, int64_t count, int32_t dev
   return ARG_OK;
 }
 
-// The weights and gradients of an optimizer's step: weights of the descriptors' types, gradients
-// fp32 or bf16, each of sizes[i] elements; their addresses (a weight's storage may have been
-// exchanged since the last step) and the gradients' types go into the descriptors.  Returns 0,
-// or 8 i + what is wrong with gradient i, or 8 (count + i) + what is wrong with weight i (the
-// descriptors before it are filled then, and no step has been made).
-MOET_HOST int64_t moet_read_step(PyObject* grads, PyObject* weights, int64_t count,
-                                 int32_t device, const int64_t* sizes,
-                                 moet_adamw_tensor* descriptors) {
+namespace {
+
+// Tensor i of a step's list: its address as the step finds it (a storage may have been exchanged
+// since the last one), noting whether it moved.
+template <class T>
+int take(PyObject* list, int64_t i, int type, int device, int64_t n, T** out, bool* moved) {
+  PyObject* o = item(list, i);
+  if (!THPVariable_Check(o)) return ARG_TYPE;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (type_of(t) != type) return ARG_TYPE;
+  if (const int bad = check(t, device, n, false)) return bad;
+  T* p = static_cast<T*>(t.data_ptr());
+  *moved |= p != *out;
+  *out = p;
+  return ARG_OK;
+}
+
+}  // namespace
+
+// The tensors of an optimizer's step: gradients (fp32 or bf16, of sizes[i] elements), weights of
+// the descriptors' types, and `states`, a tuple of the lists m, v, m_scale, v_scale and master
+// (None where there is none; () for none at all: the descriptors keep theirs).  Their addresses
+// and the gradients' types go into the descriptors; *moved is set if an address other than a
+// gradient's changed.  Returns 0, or 8 (j count + i) + what is wrong with tensor i of list j:
+// gradients, weights, then the states' five (the descriptors before it are filled then, and no
+// step has been made).
+MOET_HOST int64_t moet_read_step(PyObject* grads, PyObject* weights, PyObject* states,
+                                 int64_t count, int32_t device, const int64_t* sizes,
+                                 moet_adamw_tensor* descriptors, int32_t* moved) {
+  enum { M = 0, V = 1, M_SCALE = 2, V_SCALE = 3, MASTER = 4, LISTS = 5 };
+  PyObject* list[LISTS] = {};
   if (length(grads) != count) return ARG_LIST;
   if (length(weights) != count) return 8 * count + ARG_LIST;
+  if (length(states) == LISTS) {
+    for (int64_t j = 0; j < LISTS; ++j) {
+      list[j] = item(states, j) == Py_None ? nullptr : item(states, j);
+      if (list[j] && length(list[j]) != count) return 8 * (j + 2) * count + ARG_LIST;
+    }
+  }
   int64_t at = 0;
+  bool changed = false;
   try {
     for (int64_t i = 0; i < count; ++i) {
+      moet_adamw_tensor& d = descriptors[i];
+      const int64_t n = sizes[i], blocks = (n + MOET_ADAMW_BLOCK - 1) / MOET_ADAMW_BLOCK;
       at = 8 * i;
       PyObject* o = item(grads, i);
       if (!THPVariable_Check(o)) return at + ARG_TYPE;
       const at::Tensor& g = THPVariable_Unpack(o);
       const int type = type_of(g);
       if (type != MOET_F32 && type != MOET_BF16) return at + ARG_TYPE;
-      if (const int bad = check(g, device, sizes[i], false)) return at + bad;
+      if (const int bad = check(g, device, n, false)) return at + bad;
+      d.g = g.const_data_ptr();
+      d.g_dtype = type;
       at = 8 * (count + i);
-      o = item(weights, i);
-      if (!THPVariable_Check(o)) return at + ARG_TYPE;
-      const at::Tensor& p = THPVariable_Unpack(o);
-      if (type_of(p) != descriptors[i].p_dtype) return at + ARG_TYPE;
-      if (const int bad = check(p, device, sizes[i], false)) return at + bad;
-      descriptors[i].g = g.const_data_ptr();
-      descriptors[i].g_dtype = type;
-      descriptors[i].p = p.data_ptr();
+      if (const int bad = take(weights, i, d.p_dtype, device, n, &d.p, &changed)) return at + bad;
+      for (int j = 0; j < LISTS; ++j) {
+        if (!list[j] || (j == MASTER && item(list[j], i) == Py_None)) continue;
+        at = 8 * ((j + 2) * count + i);
+        int bad = ARG_OK;
+        switch (j) {
+          case M: bad = take(list[j], i, d.state_dtype, device, n, &d.m, &changed); break;
+          case V: bad = take(list[j], i, d.state_dtype, device, n, &d.v, &changed); break;
+          case M_SCALE: bad = take(list[j], i, MOET_F32, device, blocks, &d.m_scale, &changed); break;
+          case V_SCALE: bad = take(list[j], i, MOET_F32, device, blocks, &d.v_scale, &changed); break;
+          default: bad = take(list[j], i, MOET_F32, device, n, &d.master, &changed); break;
+        }
+        if (bad) return at + bad;
+      }
     }
   } catch (...) {
     return at + ARG_TYPE;
   }
+  if (changed) *moved = 1;
   return ARG_OK;
 }

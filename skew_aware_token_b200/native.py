@@ -293,8 +293,8 @@ def _args() -> ctypes.PyDLL:
         handle.moet_read_arguments.restype = handle.moet_read_step.restype = ctypes.c_int64
         handle.moet_read_arguments.argtypes = [ctypes.py_object, ctypes.c_int64, ctypes.c_int32,
                                                _VP, _VP]
-        handle.moet_read_step.argtypes = [ctypes.py_object, ctypes.py_object, ctypes.c_int64,
-                                          ctypes.c_int32, _VP, _VP]
+        handle.moet_read_step.argtypes = [ctypes.py_object] * 3 + [ctypes.c_int64, ctypes.c_int32,
+                                                                  _VP, _VP, _VP]
         _args_lib = handle
     return _args_lib
 
@@ -328,24 +328,35 @@ class Arguments:
         return out
 
 
-def read_step(grads, params, sizes, device: int, tensors) -> None:
+_STEP_LISTS = ("grads", "params", "m", "v", "m_scale", "v_scale", "master")
+
+
+def read_step(grads, params, sizes, device: int, tensors, states=()) -> bool:
     """Checks the gradients (a list or tuple of fp32 or bf16 tensors, contiguous, of sizes[i]
-    elements, on CUDA device `device`) and weights of an optimizer's step and fills their
-    addresses and the gradients' types into the MoetAdamwTensor array `tensors`.  `sizes`: a
-    ctypes array of int64."""
-    count = len(sizes)
-    rc = _args().moet_read_step(grads, params, count, device, sizes, tensors)
+    elements, on CUDA device `device`), weights and `states` (the lists m, v, m_scale, v_scale
+    and master, None for an absent one) of an optimizer's step and fills their addresses and the
+    gradients' types into the MoetAdamwTensor array `tensors`.  `sizes`: a ctypes array of int64.
+    Returns whether a weight or state has another address than `tensors` had."""
+    count, moved = len(sizes), ctypes.c_int32(0)
+    rc = _args().moet_read_step(grads, params, states, count, device, sizes, tensors,
+                                ctypes.byref(moved))
     if rc:
-        i, what = divmod(rc, 8)
-        name = f"grads[{i}]" if i < count else f"params[{i - count}]"
+        at, what = divmod(rc, 8)
+        which, i = divmod(at, count)
+        name = f"{_STEP_LISTS[which]}[{i}]"
         if what == 1:
-            raise ValueError(f"a list of {count} gradients is needed")
+            raise ValueError(f"a list of {count} "
+                             f"{'gradients' if which == 0 else _STEP_LISTS[which]} is needed")
         if what == 2:
+            if which >= 2:
+                raise TypeError(f"{name} must be a tensor of the type it had")
             raise TypeError(f"{name} must be a torch.float32 or torch.bfloat16 tensor"
-                            + (" of the type it had" if i >= count else ""))
+                            + (" of the type it had" if which else ""))
         if what == 3:
             raise TypeError(f"{name} must be on cuda:{device}")
-        raise ValueError(f"{name} must be contiguous with {sizes[i % count]} elements")
+        n = sizes[i] if which not in (4, 5) else -(-sizes[i] // MOET_ADAMW_BLOCK)
+        raise ValueError(f"{name} must be contiguous with {n} elements")
+    return bool(moved)
 
 
 def call(fn: str, *args) -> None:

@@ -267,9 +267,9 @@ class AdamW(_OnDevice):
     codes with an fp32 scale per 256 elements; `v` then holds the second moment's root).
     `master`: True keeps fp32 masters of bf16 weights, made from the weights here; or a list
     of them.  `m`, `v`, `m_scale`, `v_scale`: lists to take as states (a checkpoint's, or
-    views of a flat buffer); zeros by default.  `step`: steps that they have seen.  The
-    states stay these tensors (copy into them to restore others); a weight's storage may be
-    exchanged between steps, not its size or type.
+    views of a flat buffer); zeros by default.  `step`: steps that they have seen.  Each step
+    takes the weights and states as it finds them: their storage may be exchanged between steps
+    (`.data`), not their size or type.
 
     Steps taken and learning rate live on the device (`steps`, `lr`), so a captured step
     replays with their current values: set_lr() between replays."""
@@ -315,7 +315,7 @@ class AdamW(_OnDevice):
                          ("master", self.master)):
             if ts is not None and len(ts) != count:
                 raise ValueError(f"{name}: {len(ts)} of them for {count} parameters")
-        specs, tensors = [], []
+        specs, tensors, self._spans = [], [], []
         self._tensors = (N.MoetAdamwTensor * count)()
         for i, p in enumerate(self.params):
             if p.dtype not in (torch.float32, torch.bfloat16):
@@ -335,22 +335,30 @@ class AdamW(_OnDevice):
             e = self._tensors[i]
             e.n, e.weight_decay = sizes[i], decay[i]
             e.p_dtype, e.state_dtype = _TYPES[p.dtype], _TYPES[state]
-        spans = []
         for (name, dt, n, _), at in zip(specs, N.Arguments(dev.index, *specs).read(*tensors)):
             field, i = name[:-1].split("[")
-            setattr(self._tensors[int(i)], "p" if field == "params" else field, at)
+            field = "p" if field == "params" else field
+            setattr(self._tensors[int(i)], field, at)
             if n:
-                spans.append((at, at + n * dt.itemsize, name))
-        spans.sort()
-        for (_, end, a), (begin, _, b) in zip(spans, spans[1:]):
-            if begin < end:
-                raise ValueError(f"{a} and {b} share memory")
+                self._spans.append((int(i), field, n * dt.itemsize, name))
+        self._apart()
         self._sizes = (ctypes.c_int64 * count)(*sizes)
         self._scale_args = N.Arguments(dev.index, ("grad_scale", torch.float32, 1, False))
         self._opt = N.MoetAdamw(float(betas[0]), float(betas[1]), float(eps))
         self.lr = torch.full((4,), float(lr), device=dev)
         self.steps = torch.tensor([step, 0, 0, 0], dtype=torch.int32, device=dev)
         self._settle()
+
+    def _apart(self):
+        """Refuses weights and states that share memory."""
+        self._known_apart = False
+        spans = sorted((at, at + size, name) for at, size, name in (
+            (getattr(self._tensors[i], field), size, name)
+            for i, field, size, name in self._spans))
+        for (_, end, a), (begin, _, b) in zip(spans, spans[1:]):
+            if begin < end:
+                raise ValueError(f"{a} and {b} share memory")
+        self._known_apart = True
 
     def set_lr(self, lr: float) -> None:
         """Sets the learning rate of the steps that follow on the current stream."""
@@ -361,7 +369,10 @@ class AdamW(_OnDevice):
         fp32 device tensor that multiplies them (a clip or a loss scale's inverse); when it
         is not finite, the step is left out."""
         grads = grads if isinstance(grads, (list, tuple)) else list(grads)
-        N.read_step(grads, self.params, self._sizes, self._index, self._tensors)
+        moved = N.read_step(grads, self.params, self._sizes, self._index, self._tensors,
+                            (self.m, self.v, self.m_scale, self.v_scale, self.master))
+        if moved or not self._known_apart:
+            self._apart()
         scale = None if grad_scale is None else self._scale_args.read(grad_scale)[0]
         self._call("moet_adamw_step",
                    (self._tensors, len(self._sizes), ctypes.byref(self._opt), self.lr.data_ptr(),

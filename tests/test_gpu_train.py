@@ -697,6 +697,56 @@ def test_adamw_follows_a_weight_whose_storage_is_exchanged():
         opt.m[0] = torch.zeros(1000, device=DEV)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_follows_states_whose_storage_is_exchanged(bits):
+    """States moved to other storage between steps (an offload and back) are the ones that the
+    next step reads and writes; what they left is not touched.  A state of another size, type
+    or device is refused, and so are states that came to share memory."""
+    sizes = [1000, 300, 0]
+    ps, gs = adam_inputs(sizes, torch.bfloat16, torch.float32, seed=5)
+    build = lambda: AdamW([p.to(DEV) for p in ps], lr=LR, state_bits=bits, master=True)
+    moved, stayed, grads = build(), build(), [g.to(DEV) for g in gs]
+    names = ["params", "m", "v", "master"] + (["m_scale", "v_scale"] if bits == 8 else [])
+    raw = lambda t: t.view(torch.uint8) if t.element_size() == 1 else t
+    for turn in range(3):
+        for opt in (moved, stayed):
+            opt.step(grads)
+        for name in names:
+            for a, b in zip(getattr(moved, name), getattr(stayed, name)):
+                assert torch.equal(raw(a), raw(b)), name
+        left = []
+        for name in names:
+            for t in getattr(moved, name):
+                left.append((t.data, t.data.cpu()))
+                t.data = t.data.cpu().to(DEV)
+        moved.step(grads)
+        stayed.step(grads)
+        for old, was in left:
+            assert torch.equal(raw(old.cpu()), raw(was))
+    for name in names[1:]:
+        t = getattr(moved, name)[0]
+        keep = t.data
+        for bad, error in ((torch.zeros(keep.numel() + 1, device=DEV).to(keep.dtype), ValueError),
+                           (keep.cpu(), TypeError), (keep.to(torch.float16), TypeError)):
+            t.data = bad
+            with pytest.raises(error, match=rf"{name}\[0\]"):
+                moved.step(grads)
+        t.data = keep
+    before = moved.steps.tolist()
+    keep = moved.m[1].data
+    moved.m[1].data = moved.m[0].data[:300]
+    for _ in range(2):
+        with pytest.raises(ValueError, match="share memory"):
+            moved.step(grads)
+    moved.m[1].data = keep
+    assert moved.steps.tolist() == before
+    moved.step(grads)
+    stayed.step(grads)
+    for name in names:
+        for a, b in zip(getattr(moved, name), getattr(stayed, name)):
+            assert torch.equal(raw(a), raw(b)), name
+
+
 def test_first_use_on_another_stream():
     """An object used at once on a stream other than the one it was built on."""
     wl = workload(700, d=1024, E=64, k=8)

@@ -263,6 +263,17 @@ def test_gradient_lists_are_checked():
     assert all(not e.g for e in t)
 
 
+def test_state_lists_are_checked():
+    """A step's state lists are read with it: one of another length is named."""
+    sizes, t = (ctypes.c_int64 * 3)(5, 5, 5), (N.MoetAdamwTensor * 3)()
+    host = [torch.zeros(5) for _ in range(3)]
+    for j, name in enumerate(("m", "v", "m_scale", "v_scale", "master")):
+        states = [None] * 5
+        states[j] = host[:2]
+        with pytest.raises(ValueError, match=f"list of 3 {name} is needed"):
+            N.read_step(host, host, sizes, 0, t, tuple(states))
+
+
 # ---- the 64-bit forms, against differences ----
 def _g(seed):
     g = torch.Generator()
