@@ -108,28 +108,31 @@ class RouterLoss(_OnDevice):
                          ("o", torch.bfloat16, rows * self.cfg.d, False),
                          ("tok_row", i32, T * k, False))
         through_losses = (("dloss", f32, 2, False), x, *batch)
+        # the buffers above are read with each call's arguments, in the entry points' order:
+        # an exchanged one is written where it is, or refused
+        own = lambda name, dt=f32: (name, dt, getattr(self, name).numel(), False)
+        saved = (own("counts", i32), own("seq_info", i32), own("_lse"))
+        grads = (own("_dgates"), own("_dlogits"), own("status", i32))
         index = self._index
-        self._loss_args = N.Arguments(index, x, ids, *batch)
-        self._gate_args = N.Arguments(index, *through_gates)
-        self._dloss_args = N.Arguments(index, *through_losses)
-        self._both_args = N.Arguments(index, *through_gates, *through_losses)
-        # the addresses of the buffers above, in the entry points' order
-        self._outputs = [t.data_ptr() for t in (self.losses, self.counts, self.probs,
-                                                self.seq_info, self._lse, self.workspace,
-                                                self.status)]
-        self._saved = [t.data_ptr() for t in (self.counts, self.seq_info, self._lse)]
-        self._grads = [t.data_ptr() for t in (self._dgates, self._dlogits, self.status)]
+        self._loss_args = N.Arguments(index, x, ids, *batch, own("losses"), own("counts", i32),
+                                      own("probs"), own("seq_info", i32), own("_lse"),
+                                      own("workspace", torch.uint8), own("status", i32))
+        self._gate_args = N.Arguments(index, *through_gates, *saved, *grads)
+        self._dloss_args = N.Arguments(index, *through_losses, *saved, *grads)
+        self._both_args = N.Arguments(index, *through_gates, *through_losses, *saved, *grads)
         self._settle()
 
     def __call__(self, logits, topk_ids, token_mask=None, seq_off=None, stream=None):
         """fp32 [2]: balance loss and z loss of logits fp32 [T, E] and the router's topk_ids
         int32 [T, k].  token_mask uint8 [T] leaves tokens out; seq_off int32 [n_seq + 1] are
         the sequences' bounds (None with one sequence: the whole batch)."""
-        x, ids, mask, off = self._loss_args.read(logits, topk_ids, token_mask, seq_off)
+        x, ids, mask, off, *outputs = self._loss_args.read(
+            logits, topk_ids, token_mask, seq_off, self.losses, self.counts, self.probs,
+            self.seq_info, self._lse, self.workspace, self.status)
         if self.cfg.T == 0:  # empty tensors have no address
-            x, ids, mask = self._grads[1], self._grads[1], None
+            x, ids, mask = outputs[0], outputs[0], None
         self._call("moet_balance_loss",
-                   (self._cfg, x, ids, mask, off, self.n_seq, *self._outputs), stream)
+                   (self._cfg, x, ids, mask, off, self.n_seq, *outputs), stream)
         return self.losses
 
     def backward(self, logits=None, topk_ids=None, topk_gates=None, dloss=None, dy=None, o=None,
@@ -140,21 +143,24 @@ class RouterLoss(_OnDevice):
         The gates' gradient is in `dgates` then."""
         gates = dy is not None or o is not None or tok_row is not None
         ids = g = dy_p = o_p = row = dl = x = mask = off = None
+        own = (self.counts, self.seq_info, self._lse, self._dgates, self._dlogits, self.status)
         if gates and dloss is not None:
-            ids, g, dy_p, o_p, row, dl, x, mask, off = self._both_args.read(
-                topk_ids, topk_gates, dy, o, tok_row, dloss, logits, token_mask, seq_off)
+            ids, g, dy_p, o_p, row, dl, x, mask, off, *own = self._both_args.read(
+                topk_ids, topk_gates, dy, o, tok_row, dloss, logits, token_mask, seq_off, *own)
         elif gates:
-            ids, g, dy_p, o_p, row = self._gate_args.read(topk_ids, topk_gates, dy, o, tok_row)
+            ids, g, dy_p, o_p, row, *own = self._gate_args.read(topk_ids, topk_gates, dy, o,
+                                                                tok_row, *own)
         elif dloss is not None:
-            dl, x, mask, off = self._dloss_args.read(dloss, logits, token_mask, seq_off)
+            dl, x, mask, off, *own = self._dloss_args.read(dloss, logits, token_mask, seq_off,
+                                                           *own)
         else:
             raise ValueError("nothing to take the gradient of: give dloss, or dy, o and tok_row")
         if self.cfg.T == 0:
             return self.dlogits
-        dgates, dlogits, status = self._grads
+        counts, info, lse, dgates, dlogits, status = own
         self._call("moet_router_backward",
-                   (self._cfg, x, ids, g, dy_p, o_p, row, mask, off, self.n_seq, *self._saved, dl,
-                    dgates if gates else None, dlogits, status), stream)
+                   (self._cfg, x, ids, g, dy_p, o_p, row, mask, off, self.n_seq, counts, info, lse,
+                    dl, dgates if gates else None, dlogits, status), stream)
         return self.dlogits
 
     def clear_status(self):
@@ -206,10 +212,15 @@ class BlockNorm(_OnDevice):
         f32, rows = torch.float32, T * d
         inputs = (("h", h_dtype, rows, False), ("y", f32, rows, True), ("gate", f32, T, True),
                   ("w_post", w_dtype, d, True), ("w_next", w_dtype, d, True))
-        self._args = N.Arguments(self._index, *inputs, ("h_out", h_dtype, rows, True))
-        self._grad_args = N.Arguments(self._index, *inputs, ("dh_out", h_dtype, rows, True),
-                                      ("dx", f32, rows, True))
-        self._x = self.x.data_ptr()
+        # with the object's own buffers, in the entry points' order: an exchanged one is written
+        # where it is, or refused
+        self._args = N.Arguments(self._index, *inputs, ("h_out", h_dtype, rows, True),
+                                 ("x", torch.bfloat16, rows, True))
+        self._grad_args = N.Arguments(
+            self._index, *inputs, ("dh_out", h_dtype, rows, True), ("dx", f32, rows, True),
+            ("dh", h_dtype, rows, False), ("dy", f32, rows, True), ("dgate", f32, T, True),
+            ("dw_post", f32, d, True), ("dw_next", f32, d, True),
+            ("workspace", torch.uint8, size, False))
         self._settle()
 
     def __call__(self, h, y=None, gate=None, w_post=None, w_next=None, h_out=None, stream=None):
@@ -223,11 +234,10 @@ class BlockNorm(_OnDevice):
                 raise ValueError("gate, w_post and h_out belong to y")
         elif h_out is None:
             h_out = self.h_out
-        inputs = self._args.read(h, y, gate, w_post, w_next, h_out)
         x = None if w_next is None else self.x
+        arrays = self._args.read(h, y, gate, w_post, w_next, h_out, x)
         if self.cfg.T:
-            self._call("moet_block_norm",
-                       (*self._refs, *inputs, None if x is None else self._x), stream)
+            self._call("moet_block_norm", (*self._refs, *arrays), stream)
         return (h if y is None else h_out), x
 
     def backward(self, h_out, y=None, gate=None, w_post=None, w_next=None, dh_out=None, dx=None,
@@ -243,15 +253,13 @@ class BlockNorm(_OnDevice):
             raise ValueError("dx and w_next are given together")
         if dh_out is None and dx is None:
             raise ValueError("give dh_out, dx or both")
-        inputs = self._grad_args.read(h_out, y, gate, w_post, w_next, dh_out, dx)
         only = lambda buf, arg: None if arg is None else buf
         g = BlockNormGrads(self.dh, only(self.dy, y), only(self.dgate, gate),
                            only(self.dw_post, w_post), only(self.dw_next, w_next))
+        arrays = self._grad_args.read(h_out, y, gate, w_post, w_next, dh_out, dx, *g,
+                                      self.workspace)
         if self.cfg.T:
-            self._call("moet_block_norm_backward",
-                       (*self._refs, *inputs,
-                        *[None if t is None else t.data_ptr() for t in g],
-                        self.workspace.data_ptr()), stream)
+            self._call("moet_block_norm_backward", (*self._refs, *arrays), stream)
         else:
             for dw in (g.dw_post, g.dw_next):
                 if dw is not None:
@@ -343,7 +351,9 @@ class AdamW(_OnDevice):
                 self._spans.append((int(i), field, n * dt.itemsize, name))
         self._apart()
         self._sizes = (ctypes.c_int64 * count)(*sizes)
-        self._scale_args = N.Arguments(dev.index, ("grad_scale", torch.float32, 1, False))
+        self._step_args = N.Arguments(dev.index, ("lr", torch.float32, 1, False),
+                                      ("grad_scale", torch.float32, 1, True),
+                                      ("steps", torch.int32, 2, False))
         self._opt = N.MoetAdamw(float(betas[0]), float(betas[1]), float(eps))
         self.lr = torch.full((4,), float(lr), device=dev)
         self.steps = torch.tensor([step, 0, 0, 0], dtype=torch.int32, device=dev)
@@ -373,7 +383,7 @@ class AdamW(_OnDevice):
                             (self.m, self.v, self.m_scale, self.v_scale, self.master))
         if moved or not self._known_apart:
             self._apart()
-        scale = None if grad_scale is None else self._scale_args.read(grad_scale)[0]
+        lr, scale, steps = self._step_args.read(self.lr, grad_scale, self.steps)
         self._call("moet_adamw_step",
-                   (self._tensors, len(self._sizes), ctypes.byref(self._opt), self.lr.data_ptr(),
-                    scale, self.steps.data_ptr()), stream)
+                   (self._tensors, len(self._sizes), ctypes.byref(self._opt), lr, scale, steps),
+                   stream)

@@ -732,6 +732,14 @@ def test_adamw_follows_states_whose_storage_is_exchanged(bits):
             with pytest.raises(error, match=rf"{name}\[0\]"):
                 moved.step(grads)
         t.data = keep
+    for name, bad, error in (("steps", torch.zeros(1, dtype=torch.int32, device=DEV), ValueError),
+                             ("steps", torch.zeros(4, device=DEV), TypeError),
+                             ("lr", torch.zeros(4), TypeError), ("lr", 1e-3, TypeError)):
+        keep = getattr(moved, name)
+        setattr(moved, name, bad)
+        with pytest.raises(error, match=name):
+            moved.step(grads)
+        setattr(moved, name, keep)
     before = moved.steps.tolist()
     keep = moved.m[1].data
     moved.m[1].data = moved.m[0].data[:300]
@@ -745,6 +753,62 @@ def test_adamw_follows_states_whose_storage_is_exchanged(bits):
     for name in names:
         for a, b in zip(getattr(moved, name), getattr(stayed, name)):
             assert torch.equal(raw(a), raw(b)), name
+
+
+def test_exchanged_buffers_are_written_where_they_are():
+    """An object's own buffers that were exchanged (the attribute or its .data) are the ones that
+    the next call writes; one of another size or type is refused."""
+    T, d, E, k = 70, 512, 16, 4
+    wl = workload(T, d=d, E=E, k=k)
+    logits, ids, gates = (t.to(DEV) for t in router_inputs(T, E, k))
+    a = on_gpu(norm_inputs(T, d, torch.bfloat16, torch.float32, "all"))
+    dx = torch.randn(T, d, generator=gen(1)).to(DEV)
+    dloss = torch.ones(2, device=DEV)
+    r, n = RouterLoss(wl, device=DEV), BlockNorm(wl, train=True, device=DEV)
+    calls = {
+        r: (lambda: r(logits, ids), ("losses", "counts", "probs", "seq_info", "_lse", "workspace",
+                                     "status")),
+        n: (lambda: n(**a), ("h_out", "x")),
+    }
+    back = {
+        r: (lambda: r.backward(logits, dloss=dloss), ("counts", "seq_info", "_lse", "_dlogits",
+                                                      "_dgates", "status")),
+        n: (lambda: n.backward(a["h"], y=a["y"], gate=a["gate"], w_post=a["w_post"],
+                               w_next=a["w_next"], dx=dx),
+            ("dh", "dy", "dgate", "dw_post", "dw_next", "workspace")),
+    }
+    for table in (calls, back):
+        for obj, (go, names) in table.items():
+            go()
+            torch.cuda.synchronize()
+            want = {name: getattr(obj, name).clone() for name in names}
+            left = []
+            for i, name in enumerate(names):
+                t = getattr(obj, name)
+                left.append((t.data, t.clone()))
+                new = t.clone() if name in ("counts", "seq_info", "_lse", "status") and \
+                    table is back else torch.zeros_like(t)
+                if i % 2:
+                    t.data = new
+                else:
+                    setattr(obj, name, new)
+            for old, _ in left:
+                old.fill_(3)
+            go()
+            torch.cuda.synchronize()
+            for old, _ in left:
+                assert bool((old == 3).all())
+            for name in names:
+                if name not in ("workspace", "_dgates"):
+                    assert torch.equal(getattr(obj, name), want[name]), name
+            for name in names:
+                keep = getattr(obj, name)
+                for bad, error in ((keep.flatten()[:-1], ValueError), (keep.cpu(), TypeError),
+                                   (keep.half(), TypeError)):
+                    setattr(obj, name, bad)
+                    with pytest.raises(error, match=name):
+                        go()
+                setattr(obj, name, keep)
 
 
 def test_first_use_on_another_stream():
