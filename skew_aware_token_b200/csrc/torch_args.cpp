@@ -29,7 +29,7 @@ int type_of(const at::Tensor& t) {
 }
 
 // A strided, contiguous CUDA tensor on `device` with n elements, or with more of them in one
-// dimension when `flat` (what MoeLayer owns).
+// dimension when `flat`.
 int check(const at::Tensor& t, int device, int64_t n, bool flat) {
   if (!t.is_cuda() || t.get_device() != device) return ARG_DEVICE;
   if (t.layout() != at::kStrided || !t.is_contiguous()) return ARG_SIZE;
@@ -47,9 +47,11 @@ PyObject* item(PyObject* list, int64_t i) {
 
 }  // namespace
 
-// One argument: its element type and size, and whether None may stand for it.
+// One argument: its element type and size, whether None may stand for it (ARG_OPTIONAL), and
+// whether a longer one-dimensional buffer may (ARG_FLAT: MoeLayer's buffers are such).
+enum { ARG_OPTIONAL = 1, ARG_FLAT = 2 };
 struct moet_arg {
-  int32_t type, optional;
+  int32_t type, flags;
   int64_t n;
 };
 
@@ -66,12 +68,13 @@ MOET_HOST int64_t moet_read_arguments(PyObject* list, int64_t count, int32_t dev
       PyObject* o = item(list, i);
       out[i] = nullptr;
       if (o == Py_None) {
-        if (!args[i].optional) return 8 * i + ARG_MISSING;
+        if (!(args[i].flags & ARG_OPTIONAL)) return 8 * i + ARG_MISSING;
         continue;
       }
       if (!THPVariable_Check(o)) return 8 * i + ARG_DEVICE;
       const at::Tensor& t = THPVariable_Unpack(o);
-      if (const int bad = check(t, device, args[i].n, true)) return 8 * i + bad;
+      if (const int bad = check(t, device, args[i].n, args[i].flags & ARG_FLAT))
+        return 8 * i + bad;
       if (type_of(t) != args[i].type) return 8 * i + ARG_TYPE;
       out[i] = t.const_data_ptr();
     }

@@ -276,8 +276,11 @@ _ARG_TYPES = {torch.float32: MOET_F32, torch.bfloat16: MOET_BF16,
               torch.float8_e4m3fn: MOET_E4M3, torch.int32: 3, torch.uint8: 4}
 
 
+ARG_OPTIONAL, ARG_FLAT = 1, 2
+
+
 class _Arg(ctypes.Structure):
-    _fields_ = [("type", ctypes.c_int32), ("optional", ctypes.c_int32), ("n", ctypes.c_int64)]
+    _fields_ = [("type", ctypes.c_int32), ("flags", ctypes.c_int32), ("n", ctypes.c_int64)]
 
 
 _args_lib = None
@@ -300,15 +303,15 @@ def _args() -> ctypes.PyDLL:
 
 
 class Arguments:
-    """The tensors that a call takes: (name, dtype, elements, optional) of each.  read() checks
-    a tuple of them and returns their addresses (None for one left out): contiguous tensors of
-    that dtype on CUDA device `device` with that many elements, or flat buffers of at least as
-    many."""
+    """The tensors that a call takes: (name, dtype, elements, flags) of each.  read() checks a
+    tuple of them and returns their addresses (None for one left out, where ARG_OPTIONAL allows
+    it): contiguous tensors of that dtype on CUDA device `device` with that many elements, or,
+    with ARG_FLAT, one-dimensional buffers of more."""
 
     def __init__(self, device: int, *specs):
         self.device, self.specs = device, specs
-        self._c = (_Arg * len(specs))(*[_Arg(_ARG_TYPES[dt], bool(opt), n)
-                                        for _, dt, n, opt in specs])
+        self._c = (_Arg * len(specs))(*[_Arg(_ARG_TYPES[dt], flags, n)
+                                        for _, dt, n, flags in specs])
         self._read, self._out = _args().moet_read_arguments, _VP * len(specs)
         self._n = len(specs)
 

@@ -102,15 +102,16 @@ class RouterLoss(_OnDevice):
         self.workspace = new(size, dt=torch.uint8)
         self.status = z(4, dt=torch.int32)
         f32, i32, rows = torch.float32, torch.int32, N.moe_workspace_size(self.cfg, N.MOE_WS_ROWS)
-        batch = (("token_mask", torch.uint8, T, True), ("seq_off", i32, S + 1, S == 1))
-        x, ids = ("logits", f32, T * E, False), ("topk_ids", i32, T * k, False)
-        through_gates = (ids, ("topk_gates", f32, T * k, False), ("dy", f32, T * self.cfg.d, False),
-                         ("o", torch.bfloat16, rows * self.cfg.d, False),
-                         ("tok_row", i32, T * k, False))
-        through_losses = (("dloss", f32, 2, False), x, *batch)
+        flat, opt = N.ARG_FLAT, N.ARG_OPTIONAL  # flat: what MoeLayer hands out
+        batch = (("token_mask", torch.uint8, T, opt), ("seq_off", i32, S + 1, opt * (S == 1)))
+        x, ids = ("logits", f32, T * E, 0), ("topk_ids", i32, T * k, flat)
+        through_gates = (ids, ("topk_gates", f32, T * k, flat), ("dy", f32, T * self.cfg.d, 0),
+                         ("o", torch.bfloat16, rows * self.cfg.d, flat),
+                         ("tok_row", i32, T * k, flat))
+        through_losses = (("dloss", f32, 2, 0), x, *batch)
         # the buffers above are read with each call's arguments, in the entry points' order:
         # an exchanged one is written where it is, or refused
-        own = lambda name, dt=f32: (name, dt, getattr(self, name).numel(), False)
+        own = lambda name, dt=f32: (name, dt, getattr(self, name).numel(), 0)
         saved = (own("counts", i32), own("seq_info", i32), own("_lse"))
         grads = (own("_dgates"), own("_dlogits"), own("status", i32))
         index = self._index
@@ -210,17 +211,18 @@ class BlockNorm(_OnDevice):
             self.workspace = new(torch.uint8, size)
         self._refs = (ctypes.byref(self.cfg), ctypes.byref(self.norm))
         f32, rows = torch.float32, T * d
-        inputs = (("h", h_dtype, rows, False), ("y", f32, rows, True), ("gate", f32, T, True),
-                  ("w_post", w_dtype, d, True), ("w_next", w_dtype, d, True))
+        opt, flat = N.ARG_OPTIONAL, N.ARG_OPTIONAL | N.ARG_FLAT  # flat: what MoeLayer hands out
+        inputs = (("h", h_dtype, rows, 0), ("y", f32, rows, flat), ("gate", f32, T, opt),
+                  ("w_post", w_dtype, d, opt), ("w_next", w_dtype, d, opt))
         # with the object's own buffers, in the entry points' order: an exchanged one is written
         # where it is, or refused
-        self._args = N.Arguments(self._index, *inputs, ("h_out", h_dtype, rows, True),
-                                 ("x", torch.bfloat16, rows, True))
+        self._args = N.Arguments(self._index, *inputs, ("h_out", h_dtype, rows, opt),
+                                 ("x", torch.bfloat16, rows, opt))
         self._grad_args = N.Arguments(
-            self._index, *inputs, ("dh_out", h_dtype, rows, True), ("dx", f32, rows, True),
-            ("dh", h_dtype, rows, False), ("dy", f32, rows, True), ("dgate", f32, T, True),
-            ("dw_post", f32, d, True), ("dw_next", f32, d, True),
-            ("workspace", torch.uint8, size, False))
+            self._index, *inputs, ("dh_out", h_dtype, rows, opt), ("dx", f32, rows, flat),
+            ("dh", h_dtype, rows, 0), ("dy", f32, rows, opt), ("dgate", f32, T, opt),
+            ("dw_post", f32, d, opt), ("dw_next", f32, d, opt),
+            ("workspace", torch.uint8, size, 0))
         self._settle()
 
     def __call__(self, h, y=None, gate=None, w_post=None, w_next=None, h_out=None, stream=None):
@@ -338,7 +340,7 @@ class AdamW(_OnDevice):
                     raise ValueError("fp32 weights have no master")
                 own.append(("master", w, torch.float32, sizes[i]))
             own.append(("params", p, p.dtype, sizes[i]))
-            specs += [(f"{name}[{i}]", dt, n, False) for name, _, dt, n in own]
+            specs += [(f"{name}[{i}]", dt, n, 0) for name, _, dt, n in own]
             tensors += [t for _, t, _, _ in own]
             e = self._tensors[i]
             e.n, e.weight_decay = sizes[i], decay[i]
@@ -351,9 +353,9 @@ class AdamW(_OnDevice):
                 self._spans.append((int(i), field, n * dt.itemsize, name))
         self._apart()
         self._sizes = (ctypes.c_int64 * count)(*sizes)
-        self._step_args = N.Arguments(dev.index, ("lr", torch.float32, 1, False),
-                                      ("grad_scale", torch.float32, 1, True),
-                                      ("steps", torch.int32, 2, False))
+        self._step_args = N.Arguments(dev.index, ("lr", torch.float32, 1, N.ARG_FLAT),
+                                      ("grad_scale", torch.float32, 1, N.ARG_OPTIONAL),
+                                      ("steps", torch.int32, 2, N.ARG_FLAT))
         self._opt = N.MoetAdamw(float(betas[0]), float(betas[1]), float(eps))
         self.lr = torch.full((4,), float(lr), device=dev)
         self.steps = torch.tensor([step, 0, 0, 0], dtype=torch.int32, device=dev)

@@ -1011,6 +1011,62 @@ def test_wrong_arguments_are_refused():
             t.backward(a["h"], **bad)
 
 
+def test_longer_arguments_are_refused():
+    """A vector that is too long is refused as a short one is; MoeLayer's flat buffers, which are
+    longer than their contents, are taken."""
+    T, d, E, k = 64, 256, 8, 2
+    wl = workload(T, d=d, E=E, k=k)
+    logits, ids, gates = (t.to(DEV) for t in router_inputs(T, E, k))
+    r = RouterLoss(wl, n_seq=2, device=DEV)
+    more = lambda t, n=1: torch.cat([t.reshape(-1), t.reshape(-1)[:n]])
+    off = torch.tensor([0, 30, T], dtype=torch.int32, device=DEV)
+    three = torch.tensor([0, 20, 40, T], dtype=torch.int32, device=DEV)
+    mask = torch.ones(T, dtype=torch.uint8, device=DEV)
+    dloss = torch.ones(2, device=DEV)
+    for name, bad in (("seq_off", three), ("token_mask", more(mask)), ("logits", more(logits))):
+        with pytest.raises(ValueError, match=name):
+            r(**{**dict(logits=logits, topk_ids=ids, seq_off=off), name: bad})
+        with pytest.raises(ValueError, match=name):
+            r.backward(**{**dict(logits=logits, dloss=dloss, seq_off=off), name: bad})
+    with pytest.raises(ValueError, match="dloss"):
+        r.backward(logits, dloss=torch.ones(3, device=DEV), seq_off=off)
+    a = on_gpu(norm_inputs(T, d, torch.bfloat16, torch.float32, "all"))
+    n = BlockNorm(wl, train=True, device=DEV)
+    dx = torch.randn(T, d, device=DEV)
+    for name in ("h", "gate", "w_post", "w_next"):
+        with pytest.raises(ValueError, match=name):
+            n(**{**a, name: more(a[name])})
+    for name in ("gate", "w_post", "w_next", "dh_out"):
+        b = dict(y=a["y"], gate=a["gate"], w_post=a["w_post"], w_next=a["w_next"],
+                 dh_out=a["h"], dx=dx)
+        with pytest.raises(ValueError, match=name):
+            n.backward(a["h"], **{**b, name: more(b[name])})
+    n_p = 300
+    p = lambda dt=torch.float32: torch.zeros(n_p, dtype=dt, device=DEV)
+    z = lambda n, dt=torch.float32: [torch.zeros(n, device=DEV).to(dt)]
+    e4 = torch.float8_e4m3fn
+    for kw in (dict(m=z(301)), dict(v=z(301)), dict(state_bits=8, m=z(301, e4)),
+               dict(state_bits=8, m_scale=z(3)), dict(state_bits=8, v_scale=z(3))):
+        with pytest.raises(ValueError, match="contiguous with"):
+            AdamW([p()], **kw)
+    with pytest.raises(ValueError, match="master"):
+        AdamW([p(torch.bfloat16)], master=z(301))
+    with pytest.raises(ValueError, match="grad_scale"):
+        AdamW([p()]).step([p()], grad_scale=torch.ones(2, device=DEV))
+    # what MoeLayer owns
+    want = r(logits, ids, None, off).clone()
+    assert torch.equal(r(logits, more(ids, 7), None, off), want)
+    R_max = N.moe_workspace_size(wl, N.MOE_WS_ROWS)
+    o = torch.randn(R_max, d, generator=gen(1)).bfloat16().to(DEV)
+    rows = rows_of(ids.cpu(), E, wl.beta).to(DEV)
+    want = r.backward(topk_ids=ids, topk_gates=gates, dy=dx, o=o, tok_row=rows).clone()
+    got = r.backward(topk_ids=more(ids, 7), topk_gates=more(gates, 7), dy=dx, o=more(o, 9),
+                     tok_row=more(rows, 5))
+    assert torch.equal(got, want)
+    want = n(**a)[1].clone()
+    assert torch.equal(n(**{**a, "y": more(a["y"], 4)})[1], want)
+
+
 def test_rows_around_the_outputs_stay():
     """Guard elements around every output of the C ABI calls stay as they were."""
     T, d, E, k, G = 37, 264, 12, 3, 64
