@@ -602,6 +602,30 @@ def test_adamw(bits, pt, master, gt):
                   (2.0 ** -4 + 16 * U) * v.sqrt() + 2.0 ** -9 * sc, "root of v")
 
 
+@pytest.mark.parametrize("eps", [2e-38, 1e-30, 1e-20, 1e-16, 1e-12, 1e-8])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_small_gradients_and_eps(bits, eps):
+    """Gradients whose squares are subnormal or next to it, over every eps that is taken: the
+    step is the formula's.  v's three roundings are off by 2^-150 each there (half the smallest
+    subnormal), in the root half of that relative to v."""
+    n = 4096
+    g = torch.randn(n, generator=gen(1)).sign() * 10 ** (-16 - 4.5 * torch.rand(n, generator=gen(2)))
+    opt = AdamW([torch.zeros(n, device=DEV)], lr=1.0, betas=(B1, B2), eps=eps, weight_decay=0.0,
+                state_bits=bits)
+    for step in range(1, 4):
+        m0, v0 = opt.m[0].cpu(), opt.v[0].cpu()
+        if bits == 8:
+            m0 = R.of_8bit(m0, opt.m_scale[0].cpu())
+            v0 = R.of_8bit(v0, opt.v_scale[0].cpu()) ** 2
+        p0 = opt.params[0].double().cpu()
+        opt.step([g.to(DEV)])
+        p, m, v = R.adamw(p0, g.double(), m0.double(), v0.double(), step, 1.0, B1, B2, eps, 0.0)
+        ms = (B1 * m0.double()).abs() + ((1 - B1) * g.double()).abs()
+        up = ms / (1 - B1 ** step) / ((v / (1 - B2 ** step)).sqrt() + eps)
+        tol = U * (8 * p.abs() + 8 * p0.abs() + 48 * up) + up * 3 * 2.0 ** -150 / (2 * v) * 1.1
+        close(opt.params[0], p, tol, f"p at step {step}")
+
+
 @pytest.mark.parametrize("spread", [1.0, 8.0, 30.0])
 def test_adamw_codes_of_many_roots(spread):
     """Four million roots, spread over up to 2^30 within a block (most of e4m3's codes, its
