@@ -157,7 +157,7 @@ typedef struct moet_adamw_tensor {
 } moet_adamw_tensor;
 
 typedef struct moet_adamw {
-  double beta1, beta2, eps; /* 0 <= beta < 1; eps > 0, a normal fp32 number */
+  double beta1, beta2, eps; /* 0 <= beta < 1; 2^-126 <= eps <= 2^100 */
 } moet_adamw;
 
 /* One AdamW step over `count` tensors (a HOST array, read before the call returns):

@@ -10,6 +10,9 @@ namespace moe {
 namespace {
 
 constexpr int kMaxSeq = 1 << 20;
+// The step divides by a root plus eps with a reciprocal that is 0 from 2^126 on; a root is below
+// 2^64 (1 - beta2)^-1/2.
+constexpr float kMaxEps = 0x1p100f;
 constexpr long long kMaxTensor = 1LL << 40;
 
 int check_optional(std::initializer_list<const void*> ps) {
@@ -135,7 +138,7 @@ int moet_adamw_step(const moet_adamw_tensor* tensors, int32_t count, const moet_
                     moe_stream_t stream) {
   if (count < 0 || (count > 0 && !tensors) || !opt) return MOE_ERR_INVALID_ARG;
   if (!(opt->beta1 >= 0. && opt->beta1 < 1.) || !(opt->beta2 >= 0. && opt->beta2 < 1.) ||
-      !((float)opt->eps >= FLT_MIN) || !std::isfinite((float)opt->eps))
+      !((float)opt->eps >= FLT_MIN && (float)opt->eps <= kMaxEps))
     return MOE_ERR_INVALID_ARG;
   int rc = check_ptrs({lr, step});
   if (rc == MOE_OK) rc = check_optional({grad_scale});

@@ -185,6 +185,15 @@ def test_adamw_refusals():
     assert step(tensors(), 1, None, OK, None, OK, None) == INVALID
 
 
+@no_gpu
+def test_adamw_refuses_an_eps_without_a_reciprocal():
+    """An eps whose fp32 reciprocal the step's approximate one flushes to 0."""
+    for far in (2.0 ** 101, 1e38, 3e38):
+        opt = N.MoetAdamw(0.9, 0.9, far)
+        assert N.lib().moet_adamw_step(tensors(), 1, ctypes.byref(opt), OK, None, OK,
+                                       None) == INVALID, far
+
+
 def test_classes_refuse_the_cpu():
     from skew_aware_token_b200 import train
     wl = WORKLOADS["tiny"]
