@@ -350,12 +350,14 @@ block_norm_backward_kernel(const NormArgs a, const HT* __restrict__ h_out,
     float A = 0.f, B = 0.f;
     if (w_next) {
       A = rsqrtf(fmaf(s[0], a.inv_d, a.eps));
-      B = A * A * A * s[1] * a.inv_d;
+      // <q, h'> times A first: rms(h') |h'| is at most sqrt(d), while A^3 by itself leaves fp32
+      // (rows of zeros with eps under 1e-25, rows of 1e13)
+      B = A * (A * (A * s[1] * a.inv_d));
     }
     const float uy = fmaf(A, s[4], fmaf(-B, s[5], s[3]));
     const float ry = w_post ? rsqrtf(fmaf(s[2], a.inv_d, a.eps)) : 1.f;
     const float scale = a.out_scale * gt * ry;
-    const float back = w_post ? ry * ry * uy * a.inv_d : 0.f;
+    const float back = w_post ? ry * (ry * uy * a.inv_d) : 0.f;
     const float res = y ? a.res_scale : 1.f;
     if (gate && warp == 0 && lane == 0) dgate[t] = a.out_scale * ry * uy;
 #pragma unroll

@@ -505,6 +505,36 @@ def test_block_norm_many_rows_of_parts(T, d, ht, parts):
         assert all(torch.equal(t, f) for t, f in zip([t for t in run() if t is not None], first))
 
 
+@pytest.mark.parametrize("eps", [1e-30, 1e-6])
+def test_block_norm_gradient_of_small_and_large_rows(eps):
+    """Rows of zeros, of tiny and of huge values, with a small eps: the formula's gradients (the
+    cube of rms leaves fp32 in both directions, what it stands in does not).  Bounds as in
+    test_block_norm_gradient."""
+    scales = [0.0, 1e-18, 1e-16, 1e-8, 1.0, 1e6, 1e13, 1e15]
+    T, d = len(scales), 512
+    s = torch.tensor(scales)[:, None]
+    h, y = torch.randn(T, d, generator=gen(70)) * s, torch.randn(T, d, generator=gen(71)) * s
+    wp, wn = (1 + 0.2 * torch.randn(d, generator=gen(n)) for n in (72, 73))
+    dh_out, dx = (torch.randn(T, d, generator=gen(n)) for n in (74, 75))
+    norm = BlockNorm(workload(T, d=d), h_dtype=torch.float32, train=True, eps=eps, device=DEV)
+    g = norm.backward(h.to(DEV), y=y.to(DEV), w_post=wp.to(DEV), w_next=wn.to(DEV),
+                      dh_out=dh_out.to(DEV), dx=dx.to(DEV))
+    h, y, wp, wn, dh_out, dx = (t.double() for t in (h, y, wp, wn, dh_out, dx))
+    leaf = [t.clone().requires_grad_() for t in (h, wn, y, wp)]
+    x = R.rms_norm(leaf[0], leaf[1], eps, 0.0)
+    gh, gn = torch.autograd.grad((x * dx).sum(), leaf[:2])
+    u = dh_out + gh
+    gy, gp = torch.autograd.grad((R.rms_norm(leaf[2], leaf[3], eps, 0.0) * u).sum(), leaf[2:])
+    A, ry = (1 / torch.sqrt((t ** 2).mean(1, keepdim=True) + eps) for t in (h, y))
+    qa = (dx * wn).abs()
+    M = dh_out.abs() + A * qa + A ** 3 * h.abs() * (qa * h.abs()).mean(1, keepdim=True)
+    size = ry * M * wp.abs() + ry ** 3 * y.abs() * (M * (wp * y).abs()).mean(1, keepdim=True)
+    close(g.dh, u, 64 * U * M, "dh")
+    close(g.dy, gy, 96 * U * size, "dy")
+    close(g.dw_next, gn, 160 * U * (dx.abs() * A * h.abs()).sum(0), "dw_next")
+    close(g.dw_post, gp, 160 * U * (ry * M * y.abs()).sum(0), "dw_post")
+
+
 def test_block_norm_gradient_parts_and_in_place():
     """dh_out = None is zeros; dh may take dh_out's place (C ABI)."""
     T, d = 77, 768
