@@ -162,7 +162,7 @@ router_backward_kernel(const RouterArgs a, const float* __restrict__ logits,
     }
     float out[kEpt];
 #pragma unroll
-    for (int i = 0; i < kEpt; ++i) out[i] = p[i] * (c[i] - dot + z * l);
+    for (int i = 0; i < kEpt; ++i) out[i] = on ? p[i] * (c[i] - dot + z * l) : 0.f;
     if (dy) {
       const float mean = warp_sum(lane < a.k ? g * sum : 0.f);
       const float add = g * (sum - mean);

@@ -222,6 +222,30 @@ def test_router_gradient(T, d, E, k, off, masked):
     assert r.read_status() == 0
 
 
+@pytest.mark.parametrize("T,d,E,k", [(300, 512, 12, 4), (20, 2056, 64, 8), (40, 64, 8, 2)])
+@pytest.mark.parametrize("dloss", [(float("inf"), 1.0), (1.0, float("nan")), (0.0, float("-inf"))])
+def test_router_gradient_of_tokens_that_do_not_count(T, d, E, k, dloss):
+    """A loss gradient that is not finite (a loss scale that overflowed) reaches the tokens that
+    count, and none of the others: those have their gates' part, or zeros."""
+    wl = workload(T, d=d, E=E, k=k)
+    logits, ids, gates = (t.to(DEV) for t in router_inputs(T, E, k, seed=8))
+    mask = (torch.arange(T) % 3 > 0).to(torch.uint8).to(DEV)
+    off = torch.tensor([2, T - 4], dtype=torch.int32, device=DEV)
+    o = torch.randn(N.moe_workspace_size(wl, N.MOE_WS_ROWS), d, generator=gen(1)).bfloat16().to(DEV)
+    via = dict(dy=torch.randn(T, d, generator=gen(2)).to(DEV), o=o,
+               tok_row=rows_of(ids.cpu(), E, wl.beta).to(DEV))
+    r = RouterLoss(wl, device=DEV)
+    r(logits, ids, mask, off)
+    on = mask.bool()
+    on[:2] = on[T - 4:] = False
+    run = lambda **kw: r.backward(logits, ids, gates, token_mask=mask, seq_off=off, **kw).clone()
+    gate_part = run(**via)
+    bad = torch.tensor(dloss, device=DEV)
+    alone, both = run(dloss=bad), run(dloss=bad, **via)
+    assert bool((alone[~on] == 0).all()) and torch.equal(both[~on], gate_part[~on])
+    assert not bool(torch.isfinite(alone[on]).all(1).any())
+
+
 def test_router_gradient_bad_rows_and_repeats():
     T, d, E, k = 20, 64, 8, 3
     wl = workload(T, d=d, E=E, k=k)
