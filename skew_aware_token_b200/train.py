@@ -258,14 +258,11 @@ class BlockNorm(_OnDevice):
         only = lambda buf, arg: None if arg is None else buf
         g = BlockNormGrads(self.dh, only(self.dy, y), only(self.dgate, gate),
                            only(self.dw_post, w_post), only(self.dw_next, w_next))
-        arrays = self._grad_args.read(h_out, y, gate, w_post, w_next, dh_out, dx, *g,
-                                      self.workspace)
-        if self.cfg.T:
-            self._call("moet_block_norm_backward", (*self._refs, *arrays), stream)
-        else:
-            for dw in (g.dw_post, g.dw_next):
-                if dw is not None:
-                    dw.zero_()
+        given = (h_out, y, gate, w_post, w_next, dh_out, dx, *g, self.workspace)
+        arrays = self._grad_args.read(*given)
+        if self.cfg.T == 0:  # empty tensors have no address; the weights' gradients become 0
+            arrays = [None if t is None else a or arrays[-1] for t, a in zip(given, arrays)]
+        self._call("moet_block_norm_backward", (*self._refs, *arrays), stream)
         return g
 
 

@@ -559,6 +559,31 @@ def test_block_norm_gradient_of_small_and_large_rows(eps):
     close(g.dw_post, gp, 160 * U * (ry * M * y.abs()).sum(0), "dw_post")
 
 
+def test_block_norm_gradient_of_no_rows_goes_to_its_stream():
+    """Without rows the weights' gradients are zeros, written on the stream that is passed."""
+    d = 512
+    none, w = torch.zeros(0, d, device=DEV), torch.ones(d, device=DEV)
+    norm = BlockNorm(workload(0, d=d), h_dtype=torch.float32, train=True, device=DEV)
+    norm.dw_next.fill_(7)
+    norm.dw_post.fill_(7)
+    side = torch.cuda.Stream()
+    big = torch.empty(1 << 28, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(100):
+        big.fill_(1.0)                          # the current stream is busy
+    g = norm.backward(none, y=none, w_post=w, w_next=w, dx=none, stream=side)
+    with torch.cuda.stream(side):
+        got = [t.clone() for t in (g.dw_next, g.dw_post)]
+    side.synchronize()
+    assert all(float(t.abs().max()) == 0 for t in got)
+    norm.dw_next.fill_(7)
+    norm.backward(none, w_next=w, dx=none)      # the parts alone
+    assert float(norm.dw_next.abs().max()) == 0
+    gate = torch.zeros(0, device=DEV)
+    g = norm.backward(none, y=none, gate=gate, dh_out=none)
+    assert g.dw_post is None and g.dw_next is None and g.dgate.shape == (0,)
+
+
 def test_block_norm_gradient_parts_and_in_place():
     """dh_out = None is zeros; dh may take dh_out's place (C ABI)."""
     T, d = 77, 768
