@@ -107,7 +107,7 @@ int take(PyObject* list, int64_t i, int type, int device, int64_t n, T** out, bo
 // the descriptors' types, and `states`, a tuple of the lists m, v, m_scale, v_scale and master
 // (None where there is none; () for none at all: the descriptors keep theirs).  Their addresses
 // and the gradients' types go into the descriptors; *moved is set if an address other than a
-// gradient's changed.  Returns 0, or 8 (j count + i) + what is wrong with tensor i of list j:
+// gradient's changed, and the weights' versions are raised.  Returns 0, or 8 (j count + i) + what is wrong with tensor i of list j:
 // gradients, weights, then the states' five (the descriptors before it are filled then, and no
 // step has been made).
 MOET_HOST int64_t moet_read_step(PyObject* grads, PyObject* weights, PyObject* states,
@@ -153,6 +153,12 @@ MOET_HOST int64_t moet_read_step(PyObject* grads, PyObject* weights, PyObject* s
         }
         if (bad) return at + bad;
       }
+    }
+    // the step changes the weights behind autograd's back: a backward that saved one has to know
+    for (int64_t i = 0; i < count; ++i) {
+      at = 8 * (count + i);
+      const at::Tensor& p = THPVariable_Unpack(item(weights, i));
+      if (!p.is_inference()) p.unsafeGetTensorImpl()->bump_version();
     }
   } catch (...) {
     return at + ARG_TYPE;

@@ -339,7 +339,8 @@ def read_step(grads, params, sizes, device: int, tensors, states=()) -> bool:
     elements, on CUDA device `device`), weights and `states` (the lists m, v, m_scale, v_scale
     and master, None for an absent one) of an optimizer's step and fills their addresses and the
     gradients' types into the MoetAdamwTensor array `tensors`.  `sizes`: a ctypes array of int64.
-    Returns whether a weight or state has another address than `tensors` had."""
+    Raises the weights' autograd versions and returns whether a weight or state has another
+    address than `tensors` had."""
     count, moved = len(sizes), ctypes.c_int32(0)
     rc = _args().moet_read_step(grads, params, states, count, device, sizes, tensors,
                                 ctypes.byref(moved))

@@ -376,13 +376,14 @@ class AdamW(_OnDevice):
     def step(self, grads, grad_scale=None, stream=None) -> None:
         """One step with `grads` (fp32 or bf16, one a parameter, of its size).  `grad_scale`:
         fp32 device tensor that multiplies them (a clip or a loss scale's inverse); when it
-        is not finite, the step is left out."""
+        is not finite, the step is left out.  Autograd counts the step as a change of the
+        weights."""
         grads = grads if isinstance(grads, (list, tuple)) else list(grads)
+        lr, scale, steps = self._step_args.read(self.lr, grad_scale, self.steps)
         moved = N.read_step(grads, self.params, self._sizes, self._index, self._tensors,
                             (self.m, self.v, self.m_scale, self.v_scale, self.master))
         if moved or not self._known_apart:
             self._apart()
-        lr, scale, steps = self._step_args.read(self.lr, grad_scale, self.steps)
         self._call("moet_adamw_step",
                    (self._tensors, len(self._sizes), ctypes.byref(self._opt), lr, scale, steps),
                    stream)

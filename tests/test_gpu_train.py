@@ -914,6 +914,35 @@ def test_exchanged_buffers_are_written_where_they_are():
                 setattr(obj, name, keep)
 
 
+def test_adamw_raises_the_weights_versions():
+    """A weight that autograd saved in a forward before the step is an error in the backward
+    behind it; weights made in inference mode, which have no version, step too."""
+    p = torch.nn.Parameter(torch.ones(500, device=DEV))
+    q = torch.nn.Parameter(torch.ones(300, device=DEV).bfloat16())
+    opt = AdamW([p, q], lr=LR, master=True)
+    x = torch.randn(500, device=DEV, requires_grad=True)
+    y = (x * p).sum()
+    grads = [torch.ones(500, device=DEV), torch.ones(300, device=DEV)]
+    was = p._version, q._version
+    with pytest.raises(ValueError):
+        opt.step([grads[0], grads[0]])
+    assert (p._version, q._version) == was
+    opt.step(grads)
+    assert p._version > was[0] and q._version > was[1]
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    (x * p).sum().backward()
+    assert torch.equal(x.grad, p.detach())
+    with torch.inference_mode():
+        w = torch.ones(500, device=DEV)
+    inner = AdamW([w], lr=LR)
+    inner.step(grads[:1])
+    with torch.inference_mode():
+        inner.step(grads[:1])
+        opt.step(grads)
+    assert bool((w < 1).all()) and opt.steps.tolist()[0] == 2
+
+
 def test_first_use_on_another_stream():
     """An object used at once on a stream other than the one it was built on."""
     wl = workload(700, d=1024, E=64, k=8)
