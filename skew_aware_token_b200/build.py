@@ -9,6 +9,7 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -54,23 +55,45 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError(f"{ARGS_SOURCE} needs torch's headers: torch is not installed")
+    return spec.submodule_search_locations[0]
+
+
+def args_target() -> str:
+    """What libmoeskew_args.so reads the objects of: this interpreter's torch and its ABI."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        versions = re.findall(r"^(?:__version__|git_version) = '([^']*)'", f.read(), re.M)
+    return " ".join(["torch", *versions, "at", _torch_dir(),
+                     str(sysconfig.get_config_var("SOABI"))])
+
+
+def args_built_for() -> str | None:
+    """args_target() of the build that made libmoeskew_args.so (None: there is no such file, or
+    it does not say).  The library itself is not loaded."""
+    if not os.path.exists(ARGS_LIB):
+        return None
+    with open(ARGS_LIB, "rb") as f:
+        found = re.search(rb"moeskew_args built for \[([^\]]*)\]", f.read())
+    return found.group(1).decode() if found else None
+
+
 def _args_up_to_date() -> bool:
-    return os.path.exists(ARGS_LIB) and all(
+    return args_built_for() == args_target() and all(
         os.path.getmtime(p) <= os.path.getmtime(ARGS_LIB)
         for p in [ARGS_SOURCE] + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def _build_args() -> None:
     """libmoeskew_args.so: linked to the torch that this interpreter imports."""
-    spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError(f"{ARGS_SOURCE} needs torch's headers: torch is not installed")
-    torch_dir = spec.submodule_search_locations[0]
+    torch_dir = _torch_dir()
     include = os.path.join(torch_dir, "include")
     lib = os.path.join(torch_dir, "lib")
     tmp = ARGS_LIB + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-           "-fvisibility=hidden", "-I", INCLUDE, "-I", include, "-I",
+           "-fvisibility=hidden", f'-DMOESKEW_BUILT_FOR="{args_target()}"', "-I", INCLUDE, "-I", include, "-I",
            os.path.join(include, "torch", "csrc", "api", "include"), "-I",
            sysconfig.get_paths()["include"], ARGS_SOURCE, "-o", tmp, "-L", lib,
            "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]

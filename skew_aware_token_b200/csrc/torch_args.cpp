@@ -10,6 +10,11 @@
 
 #include "moeskew_train.h"
 
+// For the build, which reads it from the file: another torch or interpreter lays out its objects
+// in another way.
+extern "C" __attribute__((used)) const char moeskew_args_built_for[] =
+    "moeskew_args built for [" MOESKEW_BUILT_FOR "]";
+
 namespace {
 
 // What is wrong with an argument.

@@ -12,6 +12,8 @@ import re
 
 import torch
 
+from . import build
+
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoeskew.so")
 HEADER_PATH = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                            "include", "moeskew.h")
@@ -292,6 +294,10 @@ def _args() -> ctypes.PyDLL:
         if not os.path.exists(ARGS_LIB_PATH):
             raise RuntimeError(f"{ARGS_LIB_PATH} is missing: build it with "
                                "`python -m skew_aware_token_b200.build`")
+        built_for, target = build.args_built_for(), build.args_target()
+        if built_for != target:
+            raise RuntimeError(f"{ARGS_LIB_PATH} was built for [{built_for}], this is [{target}]: "
+                               "build it again with `python -m skew_aware_token_b200.build`")
         handle = ctypes.PyDLL(ARGS_LIB_PATH)  # the interpreter's lock stays held
         handle.moet_read_arguments.restype = handle.moet_read_step.restype = ctypes.c_int64
         handle.moet_read_arguments.argtypes = [ctypes.py_object, ctypes.c_int64, ctypes.c_int32,

@@ -272,6 +272,20 @@ def test_gradient_lists_are_checked():
     assert all(not e.g for e in t)
 
 
+def test_args_library_belongs_to_one_torch(monkeypatch):
+    """The library that reads torch's objects says which torch and interpreter it was built for;
+    for another one it is built again, and not loaded before that."""
+    target = B.args_target()
+    assert torch.__version__ in target and B.args_built_for() == target
+    assert B._args_up_to_date() and B.up_to_date()
+    N._args()
+    monkeypatch.setattr(B, "args_target", lambda: target.replace(torch.__version__, "1.0.0"))
+    assert not B._args_up_to_date() and not B.up_to_date()
+    monkeypatch.setattr(N, "_args_lib", None)
+    with pytest.raises(RuntimeError, match="was built for"):
+        N._args()
+
+
 def test_state_lists_are_checked():
     """A step's state lists are read with it: one of another length is named."""
     sizes, t = (ctypes.c_int64 * 3)(5, 5, 5), (N.MoetAdamwTensor * 3)()
