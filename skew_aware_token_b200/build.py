@@ -1,5 +1,6 @@
 """Builds libmoeskew.so in-tree with nvcc for sm_100a (no GPU needed to build), and beside it
-libmoeskew_args.so, the host code that reads torch tensors (g++, torch's headers).
+libmoeskew_args.so, the host code that reads torch tensors (g++, torch's headers; without them
+it is left out, and what needs it says so).
 
     python -m skew_aware_token_b200.build [--force]
 """
@@ -49,10 +50,23 @@ def _deps() -> list[str]:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not _args_up_to_date():
+    if not os.path.exists(LIB) or not (_args_left_out() or _args_up_to_date()):
         return False
     t = os.path.getmtime(LIB)
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _cxx() -> str:
+    return os.environ.get("CXX", "g++")
+
+
+def _args_left_out() -> str | None:
+    """Why libmoeskew_args.so cannot be built here, or None where it can."""
+    if importlib.util.find_spec("torch") is None:
+        return "torch is not installed"
+    if not os.path.exists(os.path.join(_torch_dir(), "include", "torch", "csrc")):
+        return "torch has no headers"
+    return None if shutil.which(_cxx()) else f"{_cxx()} is not found"
 
 
 def _torch_dir() -> str:
@@ -92,7 +106,7 @@ def _build_args() -> None:
     include = os.path.join(torch_dir, "include")
     lib = os.path.join(torch_dir, "lib")
     tmp = ARGS_LIB + ".tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+    cmd = [_cxx(), "-O2", "-std=c++17", "-fPIC", "-shared",
            "-fvisibility=hidden", f'-DMOESKEW_BUILT_FOR="{args_target()}"', "-I", INCLUDE, "-I", include, "-I",
            os.path.join(include, "torch", "csrc", "api", "include"), "-I",
            sysconfig.get_paths()["include"], ARGS_SOURCE, "-o", tmp, "-L", lib,
@@ -123,16 +137,21 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        args = ex.submit(_build_args) if force or not _args_up_to_date() else None
+        left_out = _args_left_out()
+        args = None
+        if left_out:
+            sys.stderr.write(f"{os.path.basename(ARGS_LIB)} is left out: {left_out}\n")
+        elif force or not _args_up_to_date():
+            args = ex.submit(_build_args)
         objs = list(ex.map(compile_one, _sources()))
-        if args:
-            args.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    if args:
+        args.result()
     return LIB
 
 

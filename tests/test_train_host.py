@@ -286,6 +286,35 @@ def test_args_library_belongs_to_one_torch(monkeypatch):
         N._args()
 
 
+@pytest.mark.parametrize("lacking", ["torch", "headers", "compiler", "nothing"])
+def test_the_library_builds_without_torch(monkeypatch, tmp_path, capsys, lacking):
+    """libmoeskew.so needs neither torch nor g++: without them the build makes it and leaves
+    libmoeskew_args.so out.  (Stand-ins for the compilers that write what they are asked for.)"""
+    import stat
+    for name in ("nvcc", "g++"):
+        tool = tmp_path / name
+        tool.write_text('#!/bin/sh\nwhile [ "$1" != "-o" ]; do shift; done\necho made > "$2"\n')
+        tool.chmod(tool.stat().st_mode | stat.S_IXUSR)
+    monkeypatch.setenv("NVCC", str(tmp_path / "nvcc"))
+    monkeypatch.setenv("CXX", str(tmp_path / ("none" if lacking == "compiler" else "g++")))
+    for name in ("LIB", "ARGS_LIB", "BUILD"):
+        monkeypatch.setattr(B, name, str(tmp_path / name))
+    if lacking == "torch":
+        find = B.importlib.util.find_spec
+        monkeypatch.setattr(B.importlib.util, "find_spec",
+                            lambda n: None if n == "torch" else find(n))
+    elif lacking == "headers":
+        monkeypatch.setattr(B, "_torch_dir", lambda: str(tmp_path))
+    for force in (False, True):
+        assert B.build(force=force) == B.LIB and (tmp_path / "LIB").exists()
+    out = capsys.readouterr().err
+    if lacking == "nothing":
+        assert (tmp_path / "ARGS_LIB").exists() and not out
+    else:
+        assert not (tmp_path / "ARGS_LIB").exists() and "is left out" in out
+        assert B.up_to_date()
+
+
 def test_state_lists_are_checked():
     """A step's state lists are read with it: one of another length is named."""
     sizes, t = (ctypes.c_int64 * 3)(5, 5, 5), (N.MoetAdamwTensor * 3)()
