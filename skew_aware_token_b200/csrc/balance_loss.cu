@@ -146,7 +146,10 @@ __device__ __forceinline__ void chunk_sums(const Batch& b, const Workspace& w, c
     const int to = min(end, seq_at(off, s + 1, T));
     for (int t = done + threadIdx.x; t < from; t += kThreads) lse_out[t] = 0.f;
     done = from;
-    if (to <= from) continue;
+    if (to <= from) {  // an empty one: past those like it at this token (any number of them)
+      if (off) s = max(s, last_at_or_before(off, n_seq, from, lane) - 1);
+      continue;
+    }
     done = to;
     float acc[EPL];
 #pragma unroll
