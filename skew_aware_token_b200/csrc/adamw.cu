@@ -53,7 +53,10 @@ struct Item {
   long long n;
   float wd;
 };
-// Three capacities of the parameter block, so that a few tensors do not pay for many; the
+// Three capacities of the parameter block, so that a few tensors do not pay for many: what is
+// copied at a launch costs the host alone.  A call of 8 tensors takes 7.9 us with the first
+// capacity, 9.0 with the second, 10.6 with the third, one of 100 tensors 15.8 with the second and
+// 17.5 with the third (64 as the second: 60 tensors 12.3 for 13.0, 100 tensors 17.6).  The
 // largest stays under the 32764 bytes a launch can carry.
 template <int CAP>
 struct Batch {

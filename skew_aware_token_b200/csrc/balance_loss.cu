@@ -26,7 +26,11 @@ constexpr int kChunks = 296;    // chunks a batch is cut into, at most (2 for ea
 constexpr int kMinChunk = 32;   // tokens of a chunk, at least
 
 constexpr int kCluster = 8;     // CTAs that a small batch takes in one launch
-constexpr int kSmallTokens = 256;
+// A batch is small while the cluster's chunks are the shortest ones (8 warps of up to 4 tokens
+// at a time).  One launch against two, us: 256 tokens of 8, 64, 256 experts 6.2 | 7.0, 6.6 | 6.4,
+// 6.8 | 7.9; 128 tokens 6.7 | 7.2, 6.5 | 7.2, 7.0 | 8.0; 288 tokens 7.8 | 6.7, 7.2 | 7.3,
+// 8.2 | 7.4; 512 tokens 7.4 | 7.4, 7.3 | 7.2, 8.7 | 8.0.
+constexpr int kSmallTokens = kCluster * kMinChunk;
 
 int chunk_tokens(int T) {
   const int n = T <= kSmallTokens ? kCluster : kChunks;
@@ -431,9 +435,7 @@ template <int EPL>
 cudaError_t launch(const Batch& b, const Workspace& w, const Results& r, cudaStream_t st) {
   constexpr int TPW = EPL <= 2 ? 4 : 2;
   const long long units = (long long)b.n_seq * b.n_slices;
-  // A small batch of few sequences takes one launch: 256 tokens of 8 experts 6.1 us against
-  // 8.2 us in two launches; from 512 tokens on (8.3 against 8.0 us) the chunks of 8 CTAs are
-  // too long.
+  // A small batch of few sequences takes one launch.
   if (b.T <= kSmallTokens && units <= kCluster * 4) {
     balance_small_kernel<EPL, TPW><<<kCluster, kThreads, 0, st>>>(b, w, r);
     return cudaGetLastError();
