@@ -106,7 +106,7 @@ def _build_args() -> None:
     include = os.path.join(torch_dir, "include")
     lib = os.path.join(torch_dir, "lib")
     tmp = ARGS_LIB + ".tmp"
-    cmd = [_cxx(), "-O2", "-std=c++17", "-fPIC", "-shared",
+    cmd = [_cxx(), "-O3", "-std=c++17", "-fPIC", "-shared",
            "-fvisibility=hidden", f'-DMOESKEW_BUILT_FOR="{args_target()}"', "-I", INCLUDE, "-I", include, "-I",
            os.path.join(include, "torch", "csrc", "api", "include"), "-I",
            sysconfig.get_paths()["include"], ARGS_SOURCE, "-o", tmp, "-L", lib,

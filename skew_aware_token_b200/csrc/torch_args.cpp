@@ -91,14 +91,24 @@ MOET_HOST int64_t moet_read_arguments(PyObject* list, int64_t count, int32_t dev
 
 namespace {
 
-// Tensor i of a step's list: its address as the step finds it (a storage may have been exchanged
-// since the last one), noting whether it moved.
+// A tensor of a step: its address as the step finds it (a storage may have been exchanged since
+// the last one), noting whether it moved.
 template <class T>
-int take(PyObject* list, int64_t i, int type, int device, int64_t n, T** out, bool* moved) {
-  PyObject* o = item(list, i);
+inline int take(PyObject* o, int type, int device, int64_t n, T** out, bool* moved) {
   if (!THPVariable_Check(o)) return ARG_TYPE;
   const at::Tensor& t = THPVariable_Unpack(o);
-  if (type_of(t) != type) return ARG_TYPE;
+  const c10::TensorImpl* impl = t.unsafeGetTensorImpl();
+  const caffe2::TypeMeta f32 = caffe2::TypeMeta::Make<float>(),
+                         bf16 = caffe2::TypeMeta::Make<at::BFloat16>(),
+                         e4m3 = caffe2::TypeMeta::Make<at::Float8_e4m3fn>();
+  if (impl->dtype() != (type == MOET_F32 ? f32 : type == MOET_BF16 ? bf16 : e4m3)) return ARG_TYPE;
+  if (*out && impl->has_storage() && impl->numel() == n && impl->is_contiguous()) {
+    // where the last step found it, what `check` asks has the answers of that step
+    const int64_t size = type == MOET_F32 ? 4 : type == MOET_BF16 ? 2 : 1;
+    if (static_cast<char*>(impl->unsafe_storage().mutable_data()) + impl->storage_offset() * size ==
+        reinterpret_cast<char*>(*out))
+      return ARG_OK;
+  }
   if (const int bad = check(t, device, n, false)) return bad;
   T* p = static_cast<T*>(t.data_ptr());
   *moved |= p != *out;
@@ -111,23 +121,27 @@ int take(PyObject* list, int64_t i, int type, int device, int64_t n, T** out, bo
 // The tensors of an optimizer's step: gradients (fp32 or bf16, of sizes[i] elements), weights of
 // the descriptors' types, and `states`, a tuple of the lists m, v, m_scale, v_scale and master
 // (None where there is none; () for none at all: the descriptors keep theirs).  Their addresses
-// and the gradients' types go into the descriptors; *moved is set if an address other than a
-// gradient's changed, and the weights' versions are raised.  Returns 0, or 8 (j count + i) + what is wrong with tensor i of list j:
-// gradients, weights, then the states' five (the descriptors before it are filled then, and no
-// step has been made).
+// and the gradients' types go into the descriptors, and the weights' versions are raised.  Returns
+// 0, -1 if an address other than a gradient's changed, or 8 (j count + i) + what is wrong with
+// tensor i of list j: gradients, weights, then the states' five (the descriptors before it are
+// filled then, and no step has been made).
 MOET_HOST int64_t moet_read_step(PyObject* grads, PyObject* weights, PyObject* states,
                                  int64_t count, int32_t device, const int64_t* sizes,
-                                 moet_adamw_tensor* descriptors, int32_t* moved) {
+                                 moet_adamw_tensor* descriptors) {
   enum { M = 0, V = 1, M_SCALE = 2, V_SCALE = 3, MASTER = 4, LISTS = 5 };
-  PyObject* list[LISTS] = {};
+  PyObject** list[LISTS] = {};
   if (length(grads) != count) return ARG_LIST;
   if (length(weights) != count) return 8 * count + ARG_LIST;
   if (length(states) == LISTS) {
     for (int64_t j = 0; j < LISTS; ++j) {
-      list[j] = item(states, j) == Py_None ? nullptr : item(states, j);
-      if (list[j] && length(list[j]) != count) return 8 * (j + 2) * count + ARG_LIST;
+      PyObject* l = item(states, j);
+      if (l == Py_None) continue;
+      if (length(l) != count) return 8 * (j + 2) * count + ARG_LIST;
+      list[j] = PySequence_Fast_ITEMS(l);
     }
   }
+  PyObject** const g_list = PySequence_Fast_ITEMS(grads);
+  PyObject** const p_list = PySequence_Fast_ITEMS(weights);
   int64_t at = 0;
   bool changed = false;
   try {
@@ -135,7 +149,7 @@ MOET_HOST int64_t moet_read_step(PyObject* grads, PyObject* weights, PyObject* s
       moet_adamw_tensor& d = descriptors[i];
       const int64_t n = sizes[i], blocks = (n + MOET_ADAMW_BLOCK - 1) / MOET_ADAMW_BLOCK;
       at = 8 * i;
-      PyObject* o = item(grads, i);
+      PyObject* o = g_list[i];
       if (!THPVariable_Check(o)) return at + ARG_TYPE;
       const at::Tensor& g = THPVariable_Unpack(o);
       const int type = type_of(g);
@@ -144,17 +158,17 @@ MOET_HOST int64_t moet_read_step(PyObject* grads, PyObject* weights, PyObject* s
       d.g = g.const_data_ptr();
       d.g_dtype = type;
       at = 8 * (count + i);
-      if (const int bad = take(weights, i, d.p_dtype, device, n, &d.p, &changed)) return at + bad;
+      if (const int bad = take(p_list[i], d.p_dtype, device, n, &d.p, &changed)) return at + bad;
       for (int j = 0; j < LISTS; ++j) {
-        if (!list[j] || (j == MASTER && item(list[j], i) == Py_None)) continue;
+        if (!list[j] || (j == MASTER && list[j][i] == Py_None)) continue;
         at = 8 * ((j + 2) * count + i);
         int bad = ARG_OK;
         switch (j) {
-          case M: bad = take(list[j], i, d.state_dtype, device, n, &d.m, &changed); break;
-          case V: bad = take(list[j], i, d.state_dtype, device, n, &d.v, &changed); break;
-          case M_SCALE: bad = take(list[j], i, MOET_F32, device, blocks, &d.m_scale, &changed); break;
-          case V_SCALE: bad = take(list[j], i, MOET_F32, device, blocks, &d.v_scale, &changed); break;
-          default: bad = take(list[j], i, MOET_F32, device, n, &d.master, &changed); break;
+          case M: bad = take(list[j][i], d.state_dtype, device, n, &d.m, &changed); break;
+          case V: bad = take(list[j][i], d.state_dtype, device, n, &d.v, &changed); break;
+          case M_SCALE: bad = take(list[j][i], MOET_F32, device, blocks, &d.m_scale, &changed); break;
+          case V_SCALE: bad = take(list[j][i], MOET_F32, device, blocks, &d.v_scale, &changed); break;
+          default: bad = take(list[j][i], MOET_F32, device, n, &d.master, &changed); break;
         }
         if (bad) return at + bad;
       }
@@ -162,12 +176,11 @@ MOET_HOST int64_t moet_read_step(PyObject* grads, PyObject* weights, PyObject* s
     // the step changes the weights behind autograd's back: a backward that saved one has to know
     for (int64_t i = 0; i < count; ++i) {
       at = 8 * (count + i);
-      const at::Tensor& p = THPVariable_Unpack(item(weights, i));
+      const at::Tensor& p = THPVariable_Unpack(p_list[i]);
       if (!p.is_inference()) p.unsafeGetTensorImpl()->bump_version();
     }
   } catch (...) {
     return at + ARG_TYPE;
   }
-  if (changed) *moved = 1;
-  return ARG_OK;
+  return changed ? -1 : ARG_OK;
 }

@@ -303,7 +303,7 @@ def _args() -> ctypes.PyDLL:
         handle.moet_read_arguments.argtypes = [ctypes.py_object, ctypes.c_int64, ctypes.c_int32,
                                                _VP, _VP]
         handle.moet_read_step.argtypes = [ctypes.py_object] * 3 + [ctypes.c_int64, ctypes.c_int32,
-                                                                  _VP, _VP, _VP]
+                                                                  _VP, _VP]
         _args_lib = handle
     return _args_lib
 
@@ -347,10 +347,9 @@ def read_step(grads, params, sizes, device: int, tensors, states=()) -> bool:
     gradients' types into the MoetAdamwTensor array `tensors`.  `sizes`: a ctypes array of int64.
     Raises the weights' autograd versions and returns whether a weight or state has another
     address than `tensors` had."""
-    count, moved = len(sizes), ctypes.c_int32(0)
-    rc = _args().moet_read_step(grads, params, states, count, device, sizes, tensors,
-                                ctypes.byref(moved))
-    if rc:
+    count = len(sizes)
+    rc = _args().moet_read_step(grads, params, states, count, device, sizes, tensors)
+    if rc > 0:
         at, what = divmod(rc, 8)
         which, i = divmod(at, count)
         name = f"{_STEP_LISTS[which]}[{i}]"
@@ -366,7 +365,7 @@ def read_step(grads, params, sizes, device: int, tensors, states=()) -> bool:
             raise TypeError(f"{name} must be on cuda:{device}")
         n = sizes[i] if which not in (4, 5) else -(-sizes[i] // MOET_ADAMW_BLOCK)
         raise ValueError(f"{name} must be contiguous with {n} elements")
-    return bool(moved)
+    return rc < 0
 
 
 def call(fn: str, *args) -> None:

@@ -127,13 +127,13 @@ class RouterLoss(_OnDevice):
         """fp32 [2]: balance loss and z loss of logits fp32 [T, E] and the router's topk_ids
         int32 [T, k].  token_mask uint8 [T] leaves tokens out; seq_off int32 [n_seq + 1] are
         the sequences' bounds (None with one sequence: the whole batch)."""
-        x, ids, mask, off, *outputs = self._loss_args.read(
-            logits, topk_ids, token_mask, seq_off, self.losses, self.counts, self.probs,
-            self.seq_info, self._lse, self.workspace, self.status)
+        a = self._loss_args.read(logits, topk_ids, token_mask, seq_off, self.losses, self.counts,
+                                 self.probs, self.seq_info, self._lse, self.workspace, self.status)
         if self.cfg.T == 0:  # empty tensors have no address
-            x, ids, mask = outputs[0], outputs[0], None
-        self._call("moet_balance_loss",
-                   (self._cfg, x, ids, mask, off, self.n_seq, *outputs), stream)
+            a[0] = a[1] = a[4]
+        # (taken one by one: to unpack the array costs a microsecond)
+        self._call("moet_balance_loss", (self._cfg, a[0], a[1], a[2], a[3], self.n_seq, a[4], a[5],
+                                         a[6], a[7], a[8], a[9], a[10]), stream)
         return self.losses
 
     def backward(self, logits=None, topk_ids=None, topk_gates=None, dloss=None, dy=None, o=None,
@@ -143,25 +143,24 @@ class RouterLoss(_OnDevice):
         dy (fp32 [T, d]), o (the expert output rows, bf16 [R_max, d]) and tok_row, or both.
         The gates' gradient is in `dgates` then."""
         gates = dy is not None or o is not None or tok_row is not None
-        ids = g = dy_p = o_p = row = dl = x = mask = off = None
         own = (self.counts, self.seq_info, self._lse, self._dgates, self._dlogits, self.status)
         if gates and dloss is not None:
-            ids, g, dy_p, o_p, row, dl, x, mask, off, *own = self._both_args.read(
-                topk_ids, topk_gates, dy, o, tok_row, dloss, logits, token_mask, seq_off, *own)
+            a = self._both_args.read(topk_ids, topk_gates, dy, o, tok_row, dloss, logits,
+                                     token_mask, seq_off, *own)
+            via, dl, x, mask, off, at = (a[0], a[1], a[2], a[3], a[4]), a[5], a[6], a[7], a[8], 9
         elif gates:
-            ids, g, dy_p, o_p, row, *own = self._gate_args.read(topk_ids, topk_gates, dy, o,
-                                                                tok_row, *own)
+            a = self._gate_args.read(topk_ids, topk_gates, dy, o, tok_row, *own)
+            via, dl, x, mask, off, at = (a[0], a[1], a[2], a[3], a[4]), None, None, None, None, 5
         elif dloss is not None:
-            dl, x, mask, off, *own = self._dloss_args.read(dloss, logits, token_mask, seq_off,
-                                                           *own)
+            a = self._dloss_args.read(dloss, logits, token_mask, seq_off, *own)
+            via, dl, x, mask, off, at = (None,) * 5, a[0], a[1], a[2], a[3], 4
         else:
             raise ValueError("nothing to take the gradient of: give dloss, or dy, o and tok_row")
         if self.cfg.T == 0:
             return self.dlogits
-        counts, info, lse, dgates, dlogits, status = own
         self._call("moet_router_backward",
-                   (self._cfg, x, ids, g, dy_p, o_p, row, mask, off, self.n_seq, counts, info, lse,
-                    dl, dgates if gates else None, dlogits, status), stream)
+                   (self._cfg, x, *via, mask, off, self.n_seq, a[at], a[at + 1], a[at + 2], dl,
+                    a[at + 3] if gates else None, a[at + 4], a[at + 5]), stream)
         return self.dlogits
 
     def clear_status(self):
@@ -379,11 +378,11 @@ class AdamW(_OnDevice):
         is not finite, the step is left out.  Autograd counts the step as a change of the
         weights."""
         grads = grads if isinstance(grads, (list, tuple)) else list(grads)
-        lr, scale, steps = self._step_args.read(self.lr, grad_scale, self.steps)
+        a = self._step_args.read(self.lr, grad_scale, self.steps)
         moved = N.read_step(grads, self.params, self._sizes, self._index, self._tensors,
                             (self.m, self.v, self.m_scale, self.v_scale, self.master))
         if moved or not self._known_apart:
             self._apart()
         self._call("moet_adamw_step",
-                   (self._tensors, len(self._sizes), ctypes.byref(self._opt), lr, scale, steps),
+                   (self._tensors, len(self._sizes), ctypes.byref(self._opt), a[0], a[1], a[2]),
                    stream)
