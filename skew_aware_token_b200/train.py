@@ -121,6 +121,7 @@ class RouterLoss(_OnDevice):
         self._gate_args = N.Arguments(index, *through_gates, *saved, *grads)
         self._dloss_args = N.Arguments(index, *through_losses, *saved, *grads)
         self._both_args = N.Arguments(index, *through_gates, *through_losses, *saved, *grads)
+        self._forward_ran = False
         self._settle()
 
     def __call__(self, logits, topk_ids, token_mask=None, seq_off=None, stream=None):
@@ -134,6 +135,7 @@ class RouterLoss(_OnDevice):
         # (taken one by one: to unpack the array costs a microsecond)
         self._call("moet_balance_loss", (self._cfg, a[0], a[1], a[2], a[3], self.n_seq, a[4], a[5],
                                          a[6], a[7], a[8], a[9], a[10]), stream)
+        self._forward_ran = True
         return self.losses
 
     def backward(self, logits=None, topk_ids=None, topk_gates=None, dloss=None, dy=None, o=None,
@@ -156,6 +158,8 @@ class RouterLoss(_OnDevice):
             via, dl, x, mask, off, at = (None,) * 5, a[0], a[1], a[2], a[3], 4
         else:
             raise ValueError("nothing to take the gradient of: give dloss, or dy, o and tok_row")
+        if dloss is not None and not self._forward_ran:
+            raise ValueError("the losses' gradient follows a forward call: it reads what that left")
         if self.cfg.T == 0:
             return self.dlogits
         self._call("moet_router_backward",

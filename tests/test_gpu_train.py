@@ -282,6 +282,23 @@ def test_router_gradient_of_tokens_that_do_not_count(T, d, E, k, dloss):
     assert not bool(torch.isfinite(alone[on]).all(1).any())
 
 
+def test_router_losses_gradient_wants_a_forward():
+    """Before any forward call there is nothing to take the losses' gradient of (the counts are
+    zeros then, and would give zeros); the gates' part needs none."""
+    T, d, E, k = 30, 64, 8, 2
+    wl = workload(T, d=d, E=E, k=k)
+    logits, ids, gates = (t.to(DEV) for t in router_inputs(T, E, k))
+    via = dict(dy=torch.ones(T, d, device=DEV), tok_row=rows_of(ids.cpu(), E, wl.beta).to(DEV),
+               o=torch.ones(N.moe_workspace_size(wl, N.MOE_WS_ROWS), d, device=DEV).bfloat16())
+    r, dloss = RouterLoss(wl, device=DEV), torch.ones(2, device=DEV)
+    r.backward(topk_ids=ids, topk_gates=gates, **via)
+    for kw in (dict(), dict(topk_ids=ids, topk_gates=gates, **via)):
+        with pytest.raises(ValueError, match="forward"):
+            r.backward(logits, dloss=dloss, **kw)
+    r(logits, ids)
+    assert float(r.backward(logits, dloss=dloss).abs().max()) > 0
+
+
 def test_router_gradient_bad_rows_and_repeats():
     T, d, E, k = 20, 64, 8, 3
     wl = workload(T, d=d, E=E, k=k)
