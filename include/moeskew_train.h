@@ -168,7 +168,8 @@ typedef struct moet_adamw {
  * An 8-bit block's scale is its largest |m| (or root of v) over 448; values are rounded to
  * the nearest e4m3 code, and a root above 0 never to code 0; a block whose largest is below
  * 1e-30 is stored as zeros.  An infinite or NaN gradient makes its element infinite or NaN,
- * with 8-bit states its whole block's moments.
+ * with 8-bit states its whole block's moments; a finite one whose (1 - beta2) g^2 leaves fp32
+ * makes v infinite: the weight stands still but for its decay, an 8-bit block's moments are NaN.
  *   lr         fp32 [1].
  *   grad_scale fp32 [1], or NULL: 1.  When it is infinite or NaN the step is left out:
  *              nothing is written, the step count included.

@@ -80,8 +80,7 @@ def args_target() -> str:
     """What libmoeskew_args.so reads the objects of: this interpreter's torch and its ABI."""
     with open(os.path.join(_torch_dir(), "version.py")) as f:
         versions = re.findall(r"^(?:__version__|git_version) = '([^']*)'", f.read(), re.M)
-    return " ".join(["torch", *versions, "at", _torch_dir(),
-                     str(sysconfig.get_config_var("SOABI"))])
+    return " ".join(["torch", *versions, str(sysconfig.get_config_var("SOABI"))])
 
 
 def args_built_for() -> str | None:
