@@ -14,13 +14,15 @@
 // (non-negative floats order as integers).  The moments, the scales and the roundings to
 // codes are those of IEEE operations, each rounded by itself, so the stored states are
 // reproducible outside this kernel bit for bit; the weight's root and quotient are
-// approximate ones (a few steps of fp32, below what the weight's own rounding does).
+// approximate ones (a few steps of fp32, below what the weight's own rounding does; a subnormal
+// v has the root 0 unless eps is so small that this would show).
 //
 // Bound by HBM: fp32 states 200 us for 50 M fp32 weights with bf16 gradients (26 bytes each,
 // 6.5 TB/s, a copy's rate).  With bf16 weights, fp32 gradients and 8-bit states 12 bytes an
-// element carry 46 instructions: 402 M weights take 875 us at the clocks that the power limit
-// leaves (4.86 GB: 741 us at a copy's rate).  The same accesses without the arithmetic take
-// 810 to 830 us; the two blocks copied ahead hide most of it (one ahead: 942 us, none: 960).
+// element carry 48 instructions: 403 M weights take 875 to 900 us at the clocks that the power
+// limit leaves, 830 to 840 before they fall (4.86 GB: 741 us at a copy's rate).  The same accesses
+// without the arithmetic take 810 to 830 us; the two blocks copied ahead hide most of it (one
+// ahead: 942 us, none: 960).
 // Streaming stores, wider or narrower CTAs, two or four blocks a warp at a time gave nothing or
 // cost time.
 #include <cuda_fp8.h>

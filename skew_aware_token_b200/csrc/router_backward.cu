@@ -9,6 +9,10 @@
 // rows (16-byte loads, all k rows of a column in flight together) and one stride of the
 // experts; the k products and sum_i a_i p_i leave in one reduction, after which the group's
 // threads write their experts.  Bound by HBM: k d 2 bytes of O rows and d 4 of dy a token.
+// p = e^(x - lse) takes the lse that the forward stored: its rounding is a relative error of
+// |lse| 2^-24 in p, which a second pass over the logits for their largest would not be worth.
+// The losses' part alone: 16384 tokens of 256 experts 10.0 us (34 MB, 5.1 us), of 128 experts on
+// 24 sequences 8.3 us (2.6), 256 tokens of 8 experts 2.3 us.
 // The rows' indices are read a token ahead and the logits before the rows: with the index's
 // and the logits' latency in front of the rows, 16384 tokens of 8 x 7168 took 550 us; without
 // it 356 us (2.38 GB, 6.7 TB/s: the rate of a plain copy).
