@@ -132,7 +132,8 @@ MOET_HOST int64_t moet_read_step(PyObject* grads, PyObject* weights, PyObject* s
   PyObject** list[LISTS] = {};
   if (length(grads) != count) return ARG_LIST;
   if (length(weights) != count) return 8 * count + ARG_LIST;
-  if (length(states) == LISTS) {
+  const bool with_states = length(states) == LISTS;
+  if (with_states) {
     for (int64_t j = 0; j < LISTS; ++j) {
       PyObject* l = item(states, j);
       if (l == Py_None) continue;
@@ -159,19 +160,20 @@ MOET_HOST int64_t moet_read_step(PyObject* grads, PyObject* weights, PyObject* s
       d.g_dtype = type;
       at = 8 * (count + i);
       if (const int bad = take(p_list[i], d.p_dtype, device, n, &d.p, &changed)) return at + bad;
-      for (int j = 0; j < LISTS; ++j) {
-        if (!list[j] || (j == MASTER && list[j][i] == Py_None)) continue;
+      if (!with_states) continue;
+      // one of the states: none (any more) where its list is, or a master where it is None itself
+      const auto state = [&](int64_t j, int type, int64_t size, auto** out) -> int {
         at = 8 * ((j + 2) * count + i);
-        int bad = ARG_OK;
-        switch (j) {
-          case M: bad = take(list[j][i], d.state_dtype, device, n, &d.m, &changed); break;
-          case V: bad = take(list[j][i], d.state_dtype, device, n, &d.v, &changed); break;
-          case M_SCALE: bad = take(list[j][i], MOET_F32, device, blocks, &d.m_scale, &changed); break;
-          case V_SCALE: bad = take(list[j][i], MOET_F32, device, blocks, &d.v_scale, &changed); break;
-          default: bad = take(list[j][i], MOET_F32, device, n, &d.master, &changed); break;
-        }
-        if (bad) return at + bad;
-      }
+        if (list[j] && !(j == MASTER && list[j][i] == Py_None))
+          return take(list[j][i], type, device, size, out, &changed);
+        *out = nullptr;
+        return ARG_OK;
+      };
+      if (const int bad = state(M, d.state_dtype, n, &d.m)) return at + bad;
+      if (const int bad = state(V, d.state_dtype, n, &d.v)) return at + bad;
+      if (const int bad = state(M_SCALE, MOET_F32, blocks, &d.m_scale)) return at + bad;
+      if (const int bad = state(V_SCALE, MOET_F32, blocks, &d.v_scale)) return at + bad;
+      if (const int bad = state(MASTER, MOET_F32, n, &d.master)) return at + bad;
     }
     // the step changes the weights behind autograd's back: a backward that saved one has to know
     for (int64_t i = 0; i < count; ++i) {

@@ -911,6 +911,29 @@ def test_adamw_follows_states_whose_storage_is_exchanged(bits):
             assert torch.equal(raw(a), raw(b)), name
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_without_the_states_it_had(bits):
+    """States that were dropped are not stepped at the addresses that they had: the step is
+    refused, or, without masters, made on the weights themselves."""
+    g = [torch.ones(700, device=DEV)]
+    for name in ("m", "v") + (("m_scale", "v_scale") if bits == 8 else ()):
+        opt = AdamW([torch.ones(700, device=DEV)], lr=LR, state_bits=bits)
+        opt.step(g)
+        keep = getattr(opt, name)
+        was = [t.clone().view(torch.uint8) for t in keep], opt.params[0].clone()
+        setattr(opt, name, None)
+        with pytest.raises(N.MoeError):
+            opt.step(g)
+        assert torch.equal(keep[0].view(torch.uint8), was[0][0])
+        assert torch.equal(opt.params[0], was[1]) and opt.steps.tolist()[:2] == [1, 0]
+    opt = AdamW([torch.ones(700, device=DEV).bfloat16()], lr=LR, state_bits=bits, master=True)
+    opt.step(g)
+    keep, opt.master = opt.master, None
+    was, w = keep[0].clone(), opt.params[0].clone()
+    opt.step(g)
+    assert torch.equal(keep[0], was) and not torch.equal(opt.params[0], w)
+
+
 def test_exchanged_buffers_are_written_where_they_are():
     """An object's own buffers that were exchanged (the attribute or its .data) are the ones that
     the next call writes; one of another size or type is refused."""
