@@ -129,12 +129,14 @@ constexpr int kBwdRed = 2 * 8 * 17;
 // writes a buffer again has passed the barrier of the sum between, which the others reach only
 // when they have read this one.  So one barrier a sum is enough.
 __device__ __forceinline__ float group_sum(float v, int W, int group, int warp, int lane,
-                                           float* red) {
+                                           uint32_t red) {
   v = warp_sum(v);
   if (W == 1) return v;
-  if (lane == 0) red[warp] = v;
+  if (lane == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(red + warp * 4), "f"(v) : "memory");
   asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(W * 32) : "memory");
-  return warp_sum(lane < W ? red[lane] : 0.f);
+  float s = 0.f;
+  if (lane < W) asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"(red + lane * 4) : "memory");
+  return warp_sum(s);
 }
 
 // The six sums of a row over its group of W warps, on every thread.  `red`: 8 * 17 floats.
@@ -172,8 +174,8 @@ block_norm_kernel(const NormArgs a, const HT* h, const float* __restrict__ y,
   const int groups = (blockDim.x >> 5) / a.W;
   const Array<float> ys(smem_addr(smem), blockDim.x);
   const Array<HT> hs(smem_addr(smem) + U * 16 * blockDim.x, blockDim.x);
-  float* red = reinterpret_cast<float*>(smem + U * (16 + Unit<HT>::kBytes) * blockDim.x) +
-               group * kFwdRed;
+  uint32_t red = smem_addr(smem) + U * (16 + Unit<HT>::kBytes) * blockDim.x + group * kFwdRed * 4;
+  const uint32_t both = 2 * red + kFwdRed * 2;  // two buffers: behind `red` comes both - red
   auto unit = [&](int i) { return (i * a.W + warp) * 32 + lane; };
   auto ahead = [&](int t) {
     if (t < a.T) {
@@ -188,7 +190,7 @@ block_norm_kernel(const NormArgs a, const HT* h, const float* __restrict__ y,
     commit_copies();
   };
   const int step = gridDim.x * groups;
-  int t = blockIdx.x * groups + group, turn = 0;
+  int t = blockIdx.x * groups + group;
   ahead(t);
   float wp[U][4], wn[U][4];
 #pragma unroll
@@ -217,8 +219,8 @@ block_norm_kernel(const NormArgs a, const HT* h, const float* __restrict__ y,
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             if (unit(i) < a.d4) s = fmaf(yu[i][j], yu[i][j], s);
-        s = group_sum(s, a.W, group, warp, lane, red + turn * (kFwdRed / 2));
-        turn ^= 1;
+        s = group_sum(s, a.W, group, warp, lane, red);
+        red = both - red;
         scale *= rsqrtf(fmaf(s, a.inv_d, a.eps));
       }
 #pragma unroll
@@ -241,8 +243,8 @@ block_norm_kernel(const NormArgs a, const HT* h, const float* __restrict__ y,
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           if (unit(i) < a.d4) s = fmaf(hv[i][j], hv[i][j], s);
-      s = group_sum(s, a.W, group, warp, lane, red + turn * (kFwdRed / 2));
-      turn ^= 1;
+      s = group_sum(s, a.W, group, warp, lane, red);
+      red = both - red;
       const float r = rsqrtf(fmaf(s, a.inv_d, a.eps));
 #pragma unroll
       for (int i = 0; i < U; ++i) {
